@@ -12,6 +12,13 @@
  *   minisgl_cascade_decode_attn  decode for requests sharing a prefix, prefix read once
  *   minisgl_cascade_extend_attn  extend for requests sharing a prefix, prefix pass + own rows
  *
+ * The same step over a pool that keeps K and V in 4 bits (minisgl_kv_pool_fp4):
+ *
+ *   minisgl_build_slots      page-table rows, out_loc, positions and offsets from request lengths
+ *   minisgl_store_kv_fp4     quantise this step's new K/V rows into the 4-bit pool
+ *   minisgl_load_kv_fp4      read cached rows back as packed bf16 rows (for extend attention)
+ *   minisgl_decode_attn_fp4  decode attention over the 4-bit pool
+ *
  * Sources of the definitions (page title, section):
  *   [deep-dive]  "mini-sglang 架构深度解读" (mini-sglang architecture deep dive,
  *                tinymind.me): section 6.2 MHAKVCache layout, section 3.6
@@ -416,6 +423,129 @@ int minisgl_check_indices(const int32_t *page_table, int32_t batch, int64_t pt_r
 int minisgl_check_shared_prefix(const int32_t *page_table, int32_t batch, int64_t pt_row_stride,
                                 int32_t pt_width, int32_t shared_len, const int32_t *lens,
                                 uint32_t *counts, void *stream);
+
+/*
+ * Slots of one step, from the requests' lengths [learn, paged KV pool
+ * chapter: the engine allocates the pages of [cached_len, device_len) and
+ * writes their rows into the page table; sglang: out_cache_loc, positions].
+ * Request r has C = cached_lens[r] tokens in the pool and E = extend_lens[r]
+ * new ones (E < 0 counts as 0).  Its new token t is at position p = C + t.
+ * Pages are page_size consecutive rows (page g is rows g*page_size ..), and a
+ * request owns ceil(C / page_size) of them, its last cached token's row being
+ * page_table[r, C-1].  With first(r) = the new pages of requests 0 .. r-1 and
+ * S = min(C + E, pt_width):
+ *   row(r, p) = page_table[r, C-1] + p - (C-1)          p in the page of C-1,
+ *               free_pages[first(r) + p/page_size - ceil(C/page_size)] * page_size
+ *                 + p % page_size                        otherwise;
+ *   page_table[r, p] = row(r, p),  C <= p < S (other entries are not written);
+ *   out_loc[q_offsets[r] + t] = row(r, C + t),  positions[q_offsets[r] + t] = C + t;
+ *   q_offsets[r] = E_0 + .. + E_{r-1} (batch + 1 entries);  seq_lens[r] = S;
+ *   pages_used[0] = the new pages of the whole batch.
+ * A padding request (CUDA-graph batches) has cached_lens[r] < 0: it counts as
+ * C = 0, takes no page, and all its rows are dummy_row.  dummy_row also
+ * stands for a token past pt_width, for a token whose page lies past the
+ * num_free free pages (pages_used > num_free then: the caller reads
+ * pages_used after the stream and frees pages or shortens the batch), and
+ * fills out_loc from q_offsets[batch] to total_tokens (with position 0), so
+ * that a captured step of total_tokens rows stays harmless.  Tokens past
+ * total_tokens (the lengths add up to more: a caller error) get no row.
+ *   cached_lens, extend_lens: device int32 [batch].
+ *   free_pages: device int32 [num_free], page numbers, taken in order; the
+ *     values are not checked.
+ *   page_table: device int32, row r at page_table + r*pt_row_stride.
+ *   out_loc, positions: device int32 [total_tokens];  q_offsets: [batch + 1];
+ *   seq_lens: [batch];  pages_used: [1].  No output may overlap an input
+ *   (only page_table is both).
+ * 1 <= page_size <= 2^20; batch <= 4096; pt_width and total_tokens <= 2^30;
+ * lengths above 2^30 count as 2^30.  batch == 0 writes the tail of out_loc
+ * and positions, q_offsets[0] = 0 and pages_used[0] = 0.
+ */
+int minisgl_build_slots(const int32_t *cached_lens, const int32_t *extend_lens, int32_t batch,
+                        int32_t *page_table, int64_t pt_row_stride, int32_t pt_width,
+                        const int32_t *free_pages, int32_t num_free, int32_t page_size,
+                        int32_t dummy_row, int32_t *out_loc, int32_t *positions,
+                        int32_t *q_offsets, int32_t *seq_lens, int32_t *pages_used,
+                        int32_t total_tokens, void *stream);
+
+/*
+ * The KV pool in 4 bits.  A head's K (or V) row of head_dim channels is cut
+ * into blocks of 16; a block has 16 e2m1 elements c (0, 0.5, 1, 1.5, 2, 3, 4,
+ * 6, signed) and one e4m3 scale s, and its channels stand for c * s * 2^exp
+ * (exp = k_exp or v_exp).  Two elements share a byte, the even channel in the
+ * low 4 bits:
+ *   channel c of (l, row, h) is in byte  k_data + l*data_layer_stride + row*data_row_stride + h*head_dim/2 + c/2
+ *   and its scale is byte    k_scale + l*scale_layer_stride + row*scale_row_stride + h*head_dim/16 + c/16
+ * All strides are in BYTES.  4.5 bits a channel: 3.56 times the tokens of a
+ * bf16 pool in the same memory.  k_exp and v_exp let one pool hold values
+ * outside the scales' range (2^-9 .. 448): -2 is a good choice where values
+ * are around 1; they are powers of two so that every value the pool holds is
+ * exact in bf16 (at most 6 significant bits).  data bases and strides are
+ * multiples of 16 bytes, scale bases and strides multiples of head_dim/16.
+ */
+enum { MINISGL_FP4 = 2 };
+
+typedef struct {
+    void *k_data, *v_data;       /* device: e2m1 pairs of layer 0, row 0 */
+    void *k_scale, *v_scale;     /* device: e4m3 scales of layer 0, row 0 */
+    int64_t data_layer_stride, data_row_stride;    /* bytes; row >= num_kv_heads*head_dim/2 */
+    int64_t scale_layer_stride, scale_row_stride;  /* bytes; row >= num_kv_heads*head_dim/16 */
+    int32_t num_layers;
+    int32_t num_rows;
+    int32_t num_kv_heads;        /* 1 .. 4096 */
+    int32_t head_dim;            /* 64 or 128 */
+    int32_t page_size;           /* informational, as in minisgl_kv_pool */
+    int32_t dtype;               /* MINISGL_FP4 */
+    int32_t k_exp, v_exp;        /* -64 .. 64 */
+} minisgl_kv_pool_fp4;
+
+/*
+ * store_kv into the 4-bit pool [learn, paged KV pool: store_kv passage].  For
+ * every new token i, KV head and block of 16 channels x of k[i] (and v[i]):
+ *     s = e4m3(max|x| * 2^-exp / 6),   c = e2m1(x * 2^-exp / s)
+ * both rounded to nearest, ties to even, and saturating at 448 and 6; s = 0
+ * gives c = 0 (blocks whose largest value is below 6 * 2^(exp-10) vanish);
+ * c keeps the sign of x, of a zero too.  They go to row out_loc[i].  A block
+ * that holds a NaN gets s = NaN and reads back as NaN; an infinity
+ * saturates.  Arguments as minisgl_store_kv (k, v bf16, strides in
+ * elements); tokens that share a row race as there.
+ */
+int minisgl_store_kv_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const void *k,
+                         const void *v, int64_t k_tok_stride, int64_t v_tok_stride,
+                         const int32_t *out_loc, int32_t n_tokens, void *stream);
+
+/*
+ * Rows of the 4-bit pool as packed bf16 rows: for request r < batch and
+ * j < min(lens[r], pt_width), with i = offsets[r] + j < total_tokens,
+ *     k_out[i, :, :] = the values of K row page_table[r, j], v_out likewise
+ * ([total_tokens, H_kv, head_dim], token strides in elements, each row
+ * contiguous).  The values are exact in bf16.  offsets: device int32
+ * [batch + 1], non-decreasing, offsets[0] >= 0; a request's rows end at
+ * offsets[r + 1] at the latest, and rows that no request fills are left as
+ * they were.  With k_out and v_out as the layer of a bf16 pool whose page
+ * table holds offsets[r] + j, minisgl_extend_attn attends over cached rows
+ * (minisgl_build_slots with cached_lens 0 and free pages 0, 1, 2, .. of one
+ * row makes that table).
+ */
+int minisgl_load_kv_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const int32_t *page_table,
+                        int32_t batch, int64_t pt_row_stride, int32_t pt_width,
+                        const int32_t *lens, const int32_t *offsets, int32_t total_tokens,
+                        void *k_out, void *v_out, int64_t k_tok_stride, int64_t v_tok_stride,
+                        void *stream);
+
+/*
+ * Decode attention over the 4-bit pool: the definition, arguments and limits
+ * of minisgl_decode_attn (q and out bf16, n == 0 gives out = 0) with K and V
+ * the values of the pool's rows.  Products accumulate in fp32; softmax
+ * weights are rounded to fp16 (11 bits) for the product with V.
+ * workspace: as for minisgl_decode_attn (minisgl_decode_workspace_bytes);
+ * nothing in it needs to start at zero, and calls that may run at the same
+ * time need different workspaces.
+ */
+int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const void *q,
+                            int32_t num_q_heads, const int32_t *page_table, int32_t batch,
+                            int64_t pt_row_stride, int32_t pt_width, const int32_t *seq_lens,
+                            float sm_scale, void *out, void *workspace, size_t workspace_bytes,
+                            int32_t split_tokens, void *stream);
 
 /* Message of the last error on the calling thread ("" if none). */
 const char *minisgl_last_error(void);

@@ -11,12 +11,16 @@ Entry points (same names as the C ABI):
     minisgl_extend_attn(pool, layer, q, page_table, cached_lens, extend_lens, q_offsets, sm_scale, ...)
     minisgl_rope_store_kv(pool, layer, q, k, v, positions, cos_sin_cache, out_loc)
     minisgl_check_indices(page_table, lens, num_rows, out_loc)   (debugging aid)
+    minisgl_build_slots(cached_lens, extend_lens, page_table, free_pages, page_size, dummy_row, total_tokens)
+    minisgl_store_kv_fp4(pool, layer, k, v, out_loc)                    (pool: a KVPoolFP4)
+    minisgl_load_kv_fp4(pool, layer, page_table, lens, offsets, total_tokens)
+    minisgl_decode_attn_fp4(pool, layer, q, page_table, seq_lens, sm_scale, ...)
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -30,6 +34,8 @@ __all__ = [
     "minisgl_cascade_workspace_bytes", "minisgl_store_decode_attn", "minisgl_check_indices",
     "minisgl_debug_set_pdl", "extend_work_counter", "minisgl_cascade_extend_attn",
     "minisgl_cascade_extend_workspace_bytes", "minisgl_check_shared_prefix",
+    "KVPoolFP4", "Slots", "minisgl_build_slots", "minisgl_store_kv_fp4", "minisgl_load_kv_fp4",
+    "minisgl_decode_attn_fp4", "decode_workspace_fp4", "kv_pool_fp4_bytes",
 ]
 
 EXPORTED_SYMBOLS = [
@@ -39,9 +45,11 @@ EXPORTED_SYMBOLS = [
     "minisgl_cascade_decode_attn", "minisgl_cascade_workspace_bytes", "minisgl_store_decode_attn",
     "minisgl_check_indices", "minisgl_debug_set_pdl", "minisgl_cascade_extend_attn",
     "minisgl_cascade_extend_workspace_bytes", "minisgl_check_shared_prefix",
+    "minisgl_build_slots", "minisgl_store_kv_fp4", "minisgl_load_kv_fp4", "minisgl_decode_attn_fp4",
 ]
 
 MINISGL_BF16 = 1
+MINISGL_FP4 = 2
 
 
 class MinisglError(RuntimeError):
@@ -55,6 +63,19 @@ class _PoolDesc(ctypes.Structure):
         ("num_layers", ctypes.c_int32), ("num_rows", ctypes.c_int32),
         ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
         ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
+class _PoolFP4Desc(ctypes.Structure):
+    _fields_ = [
+        ("k_data", ctypes.c_void_p), ("v_data", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("data_layer_stride", ctypes.c_int64), ("data_row_stride", ctypes.c_int64),
+        ("scale_layer_stride", ctypes.c_int64), ("scale_row_stride", ctypes.c_int64),
+        ("num_layers", ctypes.c_int32), ("num_rows", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
+        ("k_exp", ctypes.c_int32), ("v_exp", ctypes.c_int32),
     ]
 
 
@@ -111,6 +132,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.minisgl_check_shared_prefix.restype = ctypes.c_int
     lib.minisgl_debug_set_pdl.argtypes = [ctypes.c_int]
     lib.minisgl_debug_set_pdl.restype = ctypes.c_int
+    P4 = ctypes.POINTER(_PoolFP4Desc)
+    lib.minisgl_build_slots.argtypes = [vp, vp, i32, vp, i64, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp,
+                                        i32, vp]
+    lib.minisgl_build_slots.restype = ctypes.c_int
+    lib.minisgl_store_kv_fp4.argtypes = [P4, i32, vp, vp, i64, i64, vp, i32, vp]
+    lib.minisgl_store_kv_fp4.restype = ctypes.c_int
+    lib.minisgl_load_kv_fp4.argtypes = [P4, i32, vp, i32, i64, i32, vp, vp, i32, vp, vp, i64, i64, vp]
+    lib.minisgl_load_kv_fp4.restype = ctypes.c_int
+    lib.minisgl_decode_attn_fp4.argtypes = [P4, i32, vp, i32, vp, i32, i64, i32, vp, f32, vp, vp, sz, i32,
+                                            vp]
+    lib.minisgl_decode_attn_fp4.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -554,3 +586,265 @@ def minisgl_check_shared_prefix(page_table: torch.Tensor, lens: torch.Tensor, sh
                                            page_table.shape[1], int(shared_len), _ptr(lens), _ptr(counts),
                                            _stream(stream)), "check_shared_prefix")
     return counts
+
+
+# --------------------------------------------------------------------------- #
+# the 4-bit pool
+# --------------------------------------------------------------------------- #
+FP4_BLOCK = 16  # channels that share a scale
+
+
+class _On:
+    """The stream a call runs on, with the tensors' device (and a stream that
+    the caller named) made current for the call's own allocations and launches."""
+    __slots__ = ("handle", "_ctx")
+
+    def __init__(self, stream, *tensors: Optional[torch.Tensor]):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise MinisglError(f"tensors on different devices: {dev} and {t.device}")
+        self._ctx = None
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+            if torch.cuda.current_device() != dev.index:
+                self._ctx = torch.cuda.device(dev)
+        else:
+            if stream.device != dev:
+                raise MinisglError(f"stream on {stream.device}, tensors on {dev}")
+            self._ctx = torch.cuda.stream(stream)
+        self.handle = ctypes.c_void_p(stream.cuda_stream)
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _need_vec(t: torch.Tensor, name: str, n: Optional[int] = None) -> None:
+    _need(t, name, torch.int32)
+    if not t.is_contiguous() or (n is not None and t.numel() != n):
+        raise MinisglError(f"{name} must be a contiguous int32 tensor" + (f" of {n} elements" if n is not None else ""))
+
+
+def _need_table(t: torch.Tensor, n: int) -> None:
+    _need(t, "page_table", torch.int32)
+    if t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MinisglError("page_table must be [B, W] with unit column stride")
+
+
+def _pt_stride(t: torch.Tensor) -> int:
+    # the stride of a table of one row (or no column) means nothing and can be anything
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _tok_stride(t: torch.Tensor, row: int) -> int:
+    return t.stride(0) if t.shape[0] > 1 else row
+
+
+class KVPoolFP4:
+    """A paged KV pool in 4 bits (the format is in include/minisgl.h): `data`
+    uint8 (2, L, R, H_kv, d/2), two e2m1 elements to a byte, and `scales`
+    (2, L, R, H_kv, d/16), e4m3 scales as float8_e4m3fn or their uint8 bytes.
+    The rows of a layer are contiguous (H_kv, ..); the axes before them may have
+    any strides.  k_exp, v_exp: the power of two that K and V values are
+    multiplied with, one int or one per layer.  Caller-owned device memory; a
+    new pool's bytes should be zero (KVPoolFP4.zeros makes one)."""
+
+    def __init__(self, data: torch.Tensor, scales: torch.Tensor, page_size: int = 1,
+                 k_exp: Union[int, Sequence[int]] = 0, v_exp: Union[int, Sequence[int]] = 0):
+        if data.dim() != 5 or data.shape[0] != 2:
+            raise MinisglError("pool data must have shape (2, L, R, H_kv, d/2)")
+        _need(data, "pool data", torch.uint8)
+        if scales.dtype == torch.float8_e4m3fn:
+            scales = scales.view(torch.uint8)
+        _need(scales, "pool scales", torch.uint8)
+        _, L, R, H, half = data.shape
+        d = 2 * half
+        if tuple(scales.shape) != (2, L, R, H, d // FP4_BLOCK):
+            raise MinisglError("pool scales must have shape (2, L, R, H_kv, d/16)")
+        if scales.device != data.device:
+            raise MinisglError("pool data and scales on different devices")
+        for t in (data, scales):
+            if t.stride(4) != 1 or (H > 1 and t.stride(3) != t.shape[4]):
+                raise MinisglError("pool rows must be (H_kv, ..) contiguous")
+        self.data, self.scales, self.page_size = data, scales, page_size
+        self.num_layers, self.num_rows, self.num_kv_heads, self.head_dim = L, R, H, d
+        exps = []
+        for e, nm in ((k_exp, "k_exp"), (v_exp, "v_exp")):
+            e = [int(e)] * L if isinstance(e, int) else [int(x) for x in e]
+            if len(e) != L or any(x < -64 or x > 64 for x in e):
+                raise MinisglError(f"{nm} must be one int or one per layer, in [-64, 64]")
+            exps.append(e)
+        self.k_exp, self.v_exp = exps
+        at = {p: _PoolFP4Desc(
+            k_data=data.data_ptr(), v_data=data.data_ptr() + data.stride(0),
+            k_scale=scales.data_ptr(), v_scale=scales.data_ptr() + scales.stride(0),
+            data_layer_stride=data.stride(1), data_row_stride=data.stride(2),
+            scale_layer_stride=scales.stride(1), scale_row_stride=scales.stride(2),
+            num_layers=L, num_rows=R, num_kv_heads=H, head_dim=d, page_size=page_size,
+            dtype=MINISGL_FP4, k_exp=p[0], v_exp=p[1]) for p in set(zip(*exps))}
+        self._by_layer = [at[p] for p in zip(*exps)]
+
+    @classmethod
+    def zeros(cls, num_layers: int, num_rows: int, num_kv_heads: int, head_dim: int, page_size: int = 1,
+              k_exp: Union[int, Sequence[int]] = 0, v_exp: Union[int, Sequence[int]] = 0,
+              device=None) -> "KVPoolFP4":
+        shape = (2, num_layers, num_rows, num_kv_heads)
+        device = device or "cuda"
+        return cls(torch.zeros(shape + (head_dim // 2,), dtype=torch.uint8, device=device),
+                   torch.zeros(shape + (head_dim // FP4_BLOCK,), dtype=torch.uint8, device=device),
+                   page_size, k_exp, v_exp)
+
+    def _desc(self, layer: int):
+        if not 0 <= layer < self.num_layers:
+            raise MinisglError(f"layer {layer} outside [0, {self.num_layers})")
+        return ctypes.byref(self._by_layer[layer])
+
+
+def kv_pool_fp4_bytes(num_layers: int, num_kv_heads: int, head_dim: int, num_tokens: int) -> int:
+    """Bytes a 4-bit pool needs to hold num_tokens token rows in every layer, K and V."""
+    return 2 * num_layers * num_kv_heads * (head_dim // 2 + head_dim // FP4_BLOCK) * num_tokens
+
+
+class Slots(NamedTuple):
+    """What minisgl_build_slots writes besides the page table (int32 CUDA tensors)."""
+    out_loc: torch.Tensor     # [total_tokens] row of each new token
+    positions: torch.Tensor   # [total_tokens] position of each new token
+    q_offsets: torch.Tensor   # [B + 1] exclusive prefix sum of extend_lens
+    seq_lens: torch.Tensor    # [B] cached_lens + extend_lens
+    pages_used: torch.Tensor  # [1] new pages the batch needs
+
+    @staticmethod
+    def empty(batch: int, total_tokens: int, device=None) -> "Slots":
+        return Slots(*(torch.empty(n, dtype=torch.int32, device=device or "cuda")
+                       for n in (total_tokens, total_tokens, batch + 1, batch, 1)))
+
+
+def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, page_table: torch.Tensor,
+                        free_pages: torch.Tensor, page_size: int, dummy_row: int, total_tokens: int,
+                        out: Optional[Slots] = None, stream=None) -> Slots:
+    """Give every new token of the batch a row: requests with cached_lens[r]
+    tokens in the pool get extend_lens[r] more, in pages taken from free_pages
+    in order.  Writes page_table [B, W] in place and returns the step's Slots
+    (into `out` if given).  cached_lens[r] < 0 marks a padding request, whose
+    rows are dummy_row.  pages_used > len(free_pages) says that pages ran out
+    (the tokens without one are on dummy_row)."""
+    lib = load_library()
+    B = cached_lens.numel()
+    _need_vec(cached_lens, "cached_lens")
+    _need_vec(extend_lens, "extend_lens", B)
+    _need_vec(free_pages, "free_pages")
+    _need_table(page_table, B)
+    total = int(total_tokens)
+    if total < 0:
+        raise MinisglError("total_tokens must not be negative")
+    given = () if out is None else tuple(out)
+    if out is not None:
+        for t, nm, n in zip(out, Slots._fields, (total, total, B + 1, B, 1)):
+            _need_vec(t, nm, n)
+    with _On(stream, cached_lens, extend_lens, page_table, free_pages, *given) as st:
+        if out is None:
+            out = Slots.empty(B, total, cached_lens.device)
+        _check(lib.minisgl_build_slots(_ptr(cached_lens), _ptr(extend_lens), B, _ptr(page_table),
+                                       _pt_stride(page_table), page_table.shape[1], _ptr(free_pages),
+                                       free_pages.numel(), int(page_size), int(dummy_row), _ptr(out.out_loc),
+                                       _ptr(out.positions), _ptr(out.q_offsets), _ptr(out.seq_lens),
+                                       _ptr(out.pages_used), total, st), "build_slots")
+    return out
+
+
+def minisgl_store_kv_fp4(pool: KVPoolFP4, layer: int, k: torch.Tensor, v: torch.Tensor,
+                         out_loc: torch.Tensor, stream=None) -> None:
+    """Quantise k[i], v[i] ([n_tokens, H_kv, d] bf16) into row out_loc[i] of the 4-bit pool."""
+    lib = load_library()
+    _need(k, "k", torch.bfloat16)
+    _need(v, "v", torch.bfloat16)
+    _need_vec(out_loc, "out_loc")
+    n = out_loc.numel()
+    row = pool.num_kv_heads * pool.head_dim
+    for t, nm in ((k, "k"), (v, "v")):
+        if not _rows_ok(t, n, row):
+            raise MinisglError(f"{nm} must be [n_tokens, H_kv, d] with contiguous rows")
+    with _On(stream, pool.data, k, v, out_loc) as st:
+        _check(lib.minisgl_store_kv_fp4(pool._desc(layer), layer, _ptr(k), _ptr(v), _tok_stride(k, row),
+                                        _tok_stride(v, row), _ptr(out_loc), n, st), "store_kv_fp4")
+
+
+def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, lens: torch.Tensor,
+                        offsets: torch.Tensor, total_tokens: int, k_out: Optional[torch.Tensor] = None,
+                        v_out: Optional[torch.Tensor] = None,
+                        stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows page_table[r, :lens[r]] of the 4-bit pool as bf16, request r's from
+    row offsets[r] of k_out and v_out ([total_tokens, H_kv, d], made here if
+    not given; rows that no request fills are not written)."""
+    lib = load_library()
+    B = lens.numel()
+    _need_table(page_table, B)
+    _need_vec(lens, "lens")
+    _need_vec(offsets, "offsets", B + 1)
+    total, H, d = int(total_tokens), pool.num_kv_heads, pool.head_dim
+    if total < 0:
+        raise MinisglError("total_tokens must not be negative")
+    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is not None:
+            _need(t, nm, torch.bfloat16)
+            if not _rows_ok(t, total, H * d):
+                raise MinisglError(f"{nm} must be [total_tokens, H_kv, d] with contiguous rows")
+    with _On(stream, pool.data, page_table, lens, offsets, k_out, v_out) as st:
+        if k_out is None:
+            k_out = torch.empty((total, H, d), dtype=torch.bfloat16, device=lens.device)
+        if v_out is None:
+            v_out = torch.empty((total, H, d), dtype=torch.bfloat16, device=lens.device)
+        _check(lib.minisgl_load_kv_fp4(pool._desc(layer), layer, _ptr(page_table), B, _pt_stride(page_table),
+                                       page_table.shape[1], _ptr(lens), _ptr(offsets), total, _ptr(k_out),
+                                       _ptr(v_out), _tok_stride(k_out, H * d), _tok_stride(v_out, H * d), st),
+               "load_kv_fp4")
+    return k_out, v_out
+
+
+def decode_workspace_fp4(batch: int, num_q_heads: int, pool: KVPoolFP4, max_splits: int = 16) -> torch.Tensor:
+    """A new workspace for minisgl_decode_attn_fp4 on the pool's device.  Calls
+    that may run at the same time need different ones."""
+    return torch.empty(minisgl_decode_workspace_bytes(batch, num_q_heads, pool.num_kv_heads, pool.head_dim,
+                                                      max_splits), dtype=torch.uint8, device=pool.data.device)
+
+
+def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_table: torch.Tensor,
+                            seq_lens: torch.Tensor, sm_scale: float, out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, split_tokens: int = 0,
+                            max_splits: int = 16, stream=None) -> torch.Tensor:
+    """Decode attention of q [B, H_q, d] over each request's page_table row of
+    the 4-bit pool.  Without a workspace the call allocates its own."""
+    lib = load_library()
+    _need(q, "q", torch.bfloat16)
+    if q.dim() != 3 or not q.is_contiguous() or q.shape[2] != pool.head_dim:
+        raise MinisglError("q must be contiguous [B, H_q, head_dim]")
+    B, Hq, d = q.shape
+    _need_table(page_table, B)
+    _need_vec(seq_lens, "seq_lens", B)
+    if out is not None:
+        _need(out, "out", torch.bfloat16)
+        if out.shape != q.shape or not out.is_contiguous():
+            raise MinisglError("out must be contiguous with the shape of q")
+    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
+        raise MinisglError("workspace must be a contiguous CUDA tensor")
+    with _On(stream, pool.data, q, page_table, seq_lens, out, workspace) as st:
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            workspace = decode_workspace_fp4(B, Hq, pool, max_splits)
+        _check(lib.minisgl_decode_attn_fp4(pool._desc(layer), layer, _ptr(q), Hq, _ptr(page_table), B,
+                                           _pt_stride(page_table), page_table.shape[1], _ptr(seq_lens),
+                                           float(sm_scale), _ptr(out), _ptr(workspace),
+                                           workspace.numel() * workspace.element_size(), split_tokens, st),
+               "decode_attn_fp4")
+    return out

@@ -189,67 +189,89 @@ struct FusedStore {
     const int32_t *out_loc;
 };
 
-int decode_impl(const minisgl_kv_pool *pool, int32_t layer, const void *q, int32_t num_q_heads,
-                const int32_t *page_table, int32_t batch, int64_t pt_row_stride, int32_t pt_width,
-                const int32_t *seq_lens, float sm_scale, void *out, void *workspace,
-                size_t workspace_bytes, int32_t split_tokens, void *stream, const FusedStore *fs) {
-    if (int rc = check_pool(pool, layer, "decode_attn")) return rc;
-    if (int rc = check_heads(num_q_heads, pool->num_kv_heads, 16, "decode_attn")) return rc;
-    if (batch < 0 || batch > 4096) return fail(MINISGL_ERR_ARG, "decode_attn: batch %d outside [0, 4096]", batch);
+// The argument checks and the workspace layout that every decode call shares:
+// fills `a` except the pool's layer pointers and the fused store.  Leaves `a`
+// unfilled when batch == 0.
+int decode_args(minisgl::DecodeArgs &a, const char *who, int32_t num_kv_heads, int32_t head_dim,
+                int32_t num_rows, const void *q, int32_t num_q_heads, const int32_t *page_table,
+                int32_t batch, int64_t pt_row_stride, int32_t pt_width, const int32_t *seq_lens,
+                float sm_scale, void *out, void *workspace, size_t workspace_bytes, int32_t split_tokens) {
+    if (int rc = check_heads(num_q_heads, num_kv_heads, 16, who)) return rc;
+    if (batch < 0 || batch > 4096) return fail(MINISGL_ERR_ARG, "%s: batch %d outside [0, 4096]", who, batch);
     if (batch == 0) return MINISGL_OK;
     if (!q || !page_table || !seq_lens || !out)
-        return fail(MINISGL_ERR_ARG, "decode_attn: NULL q, page_table, seq_lens or out");
+        return fail(MINISGL_ERR_ARG, "%s: NULL q, page_table, seq_lens or out", who);
     if (!aligned16(q) || !aligned16(out))
-        return fail(MINISGL_ERR_SHAPE, "decode_attn: q and out must be 16-byte aligned");
+        return fail(MINISGL_ERR_SHAPE, "%s: q and out must be 16-byte aligned", who);
     if (pt_width < 0 || pt_row_stride < pt_width)
-        return fail(MINISGL_ERR_SHAPE, "decode_attn: need 0 <= pt_width <= pt_row_stride");
-    if (split_tokens < 0) return fail(MINISGL_ERR_ARG, "decode_attn: split_tokens < 0");
-    const int64_t tiles = (int64_t)batch * pool->num_kv_heads * ((pt_width + 15) / 16);
+        return fail(MINISGL_ERR_SHAPE, "%s: need 0 <= pt_width <= pt_row_stride", who);
+    if (split_tokens < 0) return fail(MINISGL_ERR_ARG, "%s: split_tokens < 0", who);
+    const int64_t tiles = (int64_t)batch * num_kv_heads * ((pt_width + 15) / 16);
     if (tiles >= (int64_t(1) << 31))
-        return fail(MINISGL_ERR_UNSUPPORTED, "decode_attn: batch * H_kv * width too large");
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: batch * H_kv * width too large", who);
     // the largest split count the workspace holds
     int splits = 0;
     if (workspace && ((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0)) {
         for (int s = 256; s >= 2; --s)
-            if (ws_bytes(batch, num_q_heads, pool->num_kv_heads, pool->head_dim, s) <= workspace_bytes) {
+            if (ws_bytes(batch, num_q_heads, num_kv_heads, head_dim, s) <= workspace_bytes) {
                 splits = s;
                 break;
             }
     }
     if (splits < 2)
         return fail(MINISGL_ERR_WORKSPACE,
-                    "decode_attn: workspace must be 256-byte aligned and hold >= 2 splits (%zu bytes)",
-                    ws_bytes(batch, num_q_heads, pool->num_kv_heads, pool->head_dim, 2));
-    minisgl::DecodeArgs a;
+                    "%s: workspace must be 256-byte aligned and hold >= 2 splits (%zu bytes)", who,
+                    ws_bytes(batch, num_q_heads, num_kv_heads, head_dim, 2));
     a.q = q;
-    a.k_layer = layer_ptr(pool->k_base, pool, layer);
-    a.v_layer = layer_ptr(pool->v_base, pool, layer);
-    a.row_stride = pool->row_stride;
-    a.num_rows = pool->num_rows;
+    a.k_layer = a.v_layer = nullptr;
+    a.row_stride = 0;
+    a.num_rows = num_rows;
     a.page_table = page_table;
     a.pt_stride = pt_row_stride;
     a.pt_width = pt_width;
     a.seq_lens = seq_lens;
     a.batch = batch;
     a.num_q_heads = num_q_heads;
-    a.num_kv_heads = pool->num_kv_heads;
-    a.head_dim = pool->head_dim;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
     a.sm_scale = sm_scale;
     a.out = out;
     char *ws = static_cast<char *>(workspace);
     a.split_count = reinterpret_cast<int32_t *>(ws);
-    ws += align256((size_t)batch * pool->num_kv_heads * 4);
+    ws += align256((size_t)batch * num_kv_heads * 4);
     a.ws_lse = reinterpret_cast<float *>(ws);
     ws += align256((size_t)batch * num_q_heads * splits * 4);
     a.ws_o = reinterpret_cast<float *>(ws);
     a.max_splits = splits;
     a.split_tokens = split_tokens;
     a.lse_out = nullptr;
-    a.out_loc = fs ? fs->out_loc : nullptr;
-    a.k_new = fs ? fs->k : nullptr;
-    a.v_new = fs ? fs->v : nullptr;
-    a.new_k_stride = fs ? fs->k_tok_stride : 0;
-    a.new_v_stride = fs ? fs->v_tok_stride : 0;
+    a.out_loc = nullptr;
+    a.k_new = a.v_new = nullptr;
+    a.new_k_stride = a.new_v_stride = 0;
+    return MINISGL_OK;
+}
+
+int decode_impl(const minisgl_kv_pool *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                const int32_t *page_table, int32_t batch, int64_t pt_row_stride, int32_t pt_width,
+                const int32_t *seq_lens, float sm_scale, void *out, void *workspace,
+                size_t workspace_bytes, int32_t split_tokens, void *stream, const FusedStore *fs) {
+    if (int rc = check_pool(pool, layer, "decode_attn")) return rc;
+    minisgl::DecodeArgs a;
+    if (int rc = decode_args(a, "decode_attn", pool->num_kv_heads, pool->head_dim, pool->num_rows, q,
+                             num_q_heads, page_table, batch, pt_row_stride, pt_width, seq_lens, sm_scale,
+                             out, workspace, workspace_bytes, split_tokens))
+        return rc;
+    if (batch == 0) return MINISGL_OK;
+    a.k_layer = layer_ptr(pool->k_base, pool, layer);
+    a.v_layer = layer_ptr(pool->v_base, pool, layer);
+    a.row_stride = pool->row_stride;
+    if (fs) {
+        a.out_loc = fs->out_loc;
+        a.k_new = fs->k;
+        a.v_new = fs->v;
+        a.new_k_stride = fs->k_tok_stride;
+        a.new_v_stride = fs->v_tok_stride;
+    }
     return cuda_status(minisgl::launch_decode(a, static_cast<cudaStream_t>(stream)), "decode_attn");
 }
 
@@ -670,6 +692,205 @@ int minisgl_check_shared_prefix(const int32_t *page_table, int32_t batch, int64_
     return cuda_status(minisgl::launch_check_shared_prefix(page_table, batch, pt_row_stride, shared_len, lens,
                                                            counts, static_cast<cudaStream_t>(stream)),
                        "check_shared_prefix");
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_pool_fp4(const minisgl_kv_pool_fp4 *p, int32_t layer, const char *who) {
+    if (!p) return fail(MINISGL_ERR_ARG, "%s: pool descriptor is NULL", who);
+    if (p->dtype != MINISGL_FP4) return fail(MINISGL_ERR_DTYPE, "%s: pool dtype must be fp4", who);
+    if (!p->k_data || !p->v_data || !p->k_scale || !p->v_scale)
+        return fail(MINISGL_ERR_ARG, "%s: pool base is NULL", who);
+    if (p->head_dim != 64 && p->head_dim != 128)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: head_dim %d not in {64, 128}", who, p->head_dim);
+    if (p->num_kv_heads < 1 || p->num_rows < 1 || p->num_layers < 1)
+        return fail(MINISGL_ERR_SHAPE, "%s: pool sizes must be positive", who);
+    if (p->num_kv_heads > 4096)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: num_kv_heads %d > 4096", who, p->num_kv_heads);
+    const int64_t unit = p->head_dim / 16;
+    if (p->data_row_stride < (int64_t)p->num_kv_heads * p->head_dim / 2 || p->data_row_stride % 16)
+        return fail(MINISGL_ERR_SHAPE, "%s: data_row_stride %lld must be >= H_kv*d/2 and a multiple of 16", who,
+                    (long long)p->data_row_stride);
+    if (p->scale_row_stride < p->num_kv_heads * unit || p->scale_row_stride % unit)
+        return fail(MINISGL_ERR_SHAPE, "%s: scale_row_stride %lld must be >= H_kv*d/16 and a multiple of d/16", who,
+                    (long long)p->scale_row_stride);
+    if (!aligned16(p->k_data) || !aligned16(p->v_data) || p->data_layer_stride % 16)
+        return fail(MINISGL_ERR_SHAPE, "%s: data bases and strides must be multiples of 16 bytes", who);
+    if ((reinterpret_cast<uintptr_t>(p->k_scale) | reinterpret_cast<uintptr_t>(p->v_scale)) % unit ||
+        p->scale_layer_stride % unit)
+        return fail(MINISGL_ERR_SHAPE, "%s: scale bases and strides must be multiples of d/16 bytes", who);
+    if (p->k_exp < -64 || p->k_exp > 64 || p->v_exp < -64 || p->v_exp > 64)
+        return fail(MINISGL_ERR_ARG, "%s: k_exp and v_exp must be in [-64, 64]", who);
+    if (layer < 0 || layer >= p->num_layers)
+        return fail(MINISGL_ERR_ARG, "%s: layer %d outside [0, %d)", who, layer, p->num_layers);
+    return MINISGL_OK;
+}
+
+minisgl::Fp4Layer fp4_layer(const minisgl_kv_pool_fp4 *p, int32_t layer) {
+    minisgl::Fp4Layer l;
+    l.k_data = static_cast<uint8_t *>(p->k_data) + layer * p->data_layer_stride;
+    l.v_data = static_cast<uint8_t *>(p->v_data) + layer * p->data_layer_stride;
+    l.k_scale = static_cast<uint8_t *>(p->k_scale) + layer * p->scale_layer_stride;
+    l.v_scale = static_cast<uint8_t *>(p->v_scale) + layer * p->scale_layer_stride;
+    l.data_stride = p->data_row_stride;
+    l.scale_stride = p->scale_row_stride;
+    l.num_rows = p->num_rows;
+    l.num_kv_heads = p->num_kv_heads;
+    l.head_dim = p->head_dim;
+    l.k_exp = p->k_exp;
+    l.v_exp = p->v_exp;
+    return l;
+}
+
+// Whether [a, a + na) and [b, b + nb) (in int32 elements) share memory.
+bool overlap32(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
+    if (!a || !b || na <= 0 || nb <= 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + (uintptr_t)nb * 4 && y < x + (uintptr_t)na * 4;
+}
+
+constexpr int64_t SLOT_MAX = int64_t(1) << 30;
+
+}  // namespace
+
+extern "C" {
+
+int minisgl_build_slots(const int32_t *cached_lens, const int32_t *extend_lens, int32_t batch,
+                        int32_t *page_table, int64_t pt_row_stride, int32_t pt_width,
+                        const int32_t *free_pages, int32_t num_free, int32_t page_size,
+                        int32_t dummy_row, int32_t *out_loc, int32_t *positions,
+                        int32_t *q_offsets, int32_t *seq_lens, int32_t *pages_used,
+                        int32_t total_tokens, void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_build_slots");
+    if (batch < 0 || batch > 4096) return fail(MINISGL_ERR_ARG, "build_slots: batch %d outside [0, 4096]", batch);
+    if (total_tokens < 0 || total_tokens > SLOT_MAX)
+        return fail(MINISGL_ERR_ARG, "build_slots: total_tokens %d outside [0, 2^30]", total_tokens);
+    if (num_free < 0) return fail(MINISGL_ERR_ARG, "build_slots: num_free < 0");
+    if (page_size < 1 || page_size > (1 << 20))
+        return fail(MINISGL_ERR_ARG, "build_slots: page_size %d outside [1, 2^20]", page_size);
+    if (dummy_row < 0) return fail(MINISGL_ERR_ARG, "build_slots: dummy_row < 0");
+    if (!q_offsets || !pages_used) return fail(MINISGL_ERR_ARG, "build_slots: NULL q_offsets or pages_used");
+    if (total_tokens > 0 && (!out_loc || !positions))
+        return fail(MINISGL_ERR_ARG, "build_slots: NULL out_loc or positions");
+    if (batch > 0 && (!cached_lens || !extend_lens || !page_table || !seq_lens))
+        return fail(MINISGL_ERR_ARG, "build_slots: NULL cached_lens, extend_lens, page_table or seq_lens");
+    if (num_free > 0 && !free_pages) return fail(MINISGL_ERR_ARG, "build_slots: NULL free_pages");
+    if (pt_width < 0 || pt_width > SLOT_MAX || pt_row_stride < pt_width)
+        return fail(MINISGL_ERR_SHAPE, "build_slots: need 0 <= pt_width <= pt_row_stride, pt_width <= 2^30");
+    const int64_t B = batch, T = total_tokens;
+    const int64_t table = B > 0 && pt_width > 0 ? (B - 1) * pt_row_stride + pt_width : 0;
+    const struct { const int32_t *p; int64_t n; } in[3] = {{cached_lens, B}, {extend_lens, B}, {free_pages, num_free}},
+        out[6] = {{page_table, table}, {out_loc, T}, {positions, T}, {q_offsets, B + 1}, {seq_lens, B}, {pages_used, 1}};
+    for (int i = 0; i < 6; ++i) {
+        for (const auto &x : in)
+            if (overlap32(out[i].p, out[i].n, x.p, x.n))
+                return fail(MINISGL_ERR_ARG, "build_slots: an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (overlap32(out[i].p, out[i].n, out[j].p, out[j].n))
+                return fail(MINISGL_ERR_ARG, "build_slots: two outputs overlap");
+    }
+    minisgl::SlotArgs a;
+    a.cached_lens = cached_lens;
+    a.extend_lens = extend_lens;
+    a.batch = batch;
+    a.page_table = page_table;
+    a.pt_stride = pt_row_stride;
+    a.pt_width = pt_width;
+    a.free_pages = free_pages;
+    a.num_free = num_free;
+    a.page_size = page_size;
+    a.dummy_row = dummy_row;
+    a.out_loc = out_loc;
+    a.positions = positions;
+    a.q_offsets = q_offsets;
+    a.seq_lens = seq_lens;
+    a.pages_used = pages_used;
+    a.total_tokens = total_tokens;
+    return cuda_status(minisgl::launch_build_slots(a, static_cast<cudaStream_t>(stream)), "build_slots");
+}
+
+int minisgl_store_kv_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const void *k,
+                         const void *v, int64_t k_tok_stride, int64_t v_tok_stride,
+                         const int32_t *out_loc, int32_t n_tokens, void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_store_kv_fp4");
+    if (int rc = check_pool_fp4(pool, layer, "store_kv_fp4")) return rc;
+    if (n_tokens < 0) return fail(MINISGL_ERR_ARG, "store_kv_fp4: n_tokens < 0");
+    if (n_tokens == 0) return MINISGL_OK;
+    if (!k || !v || !out_loc) return fail(MINISGL_ERR_ARG, "store_kv_fp4: NULL k, v or out_loc");
+    const int64_t row = (int64_t)pool->num_kv_heads * pool->head_dim;
+    if (!aligned16(k) || !aligned16(v))
+        return fail(MINISGL_ERR_SHAPE, "store_kv_fp4: k and v must be 16-byte aligned");
+    if (k_tok_stride < row || v_tok_stride < row || k_tok_stride % 8 || v_tok_stride % 8)
+        return fail(MINISGL_ERR_SHAPE, "store_kv_fp4: token strides must be >= H_kv*d and multiples of 8");
+    if ((int64_t)n_tokens * (row / 8) >= (int64_t(1) << 31))
+        return fail(MINISGL_ERR_UNSUPPORTED, "store_kv_fp4: n_tokens * H_kv * d too large for one call");
+    minisgl::StoreFp4Args a;
+    a.pool = fp4_layer(pool, layer);
+    a.k = k;
+    a.v = v;
+    a.k_tok_stride = k_tok_stride;
+    a.v_tok_stride = v_tok_stride;
+    a.out_loc = out_loc;
+    a.n_tokens = n_tokens;
+    return cuda_status(minisgl::launch_store_kv_fp4(a, static_cast<cudaStream_t>(stream)), "store_kv_fp4");
+}
+
+int minisgl_load_kv_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const int32_t *page_table,
+                        int32_t batch, int64_t pt_row_stride, int32_t pt_width,
+                        const int32_t *lens, const int32_t *offsets, int32_t total_tokens,
+                        void *k_out, void *v_out, int64_t k_tok_stride, int64_t v_tok_stride,
+                        void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_load_kv_fp4");
+    if (int rc = check_pool_fp4(pool, layer, "load_kv_fp4")) return rc;
+    if (batch < 0 || batch > 4096) return fail(MINISGL_ERR_ARG, "load_kv_fp4: batch %d outside [0, 4096]", batch);
+    if (total_tokens < 0) return fail(MINISGL_ERR_ARG, "load_kv_fp4: total_tokens < 0");
+    if (batch == 0 || total_tokens == 0) return MINISGL_OK;
+    if (!page_table || !lens || !offsets || !k_out || !v_out)
+        return fail(MINISGL_ERR_ARG, "load_kv_fp4: NULL pointer argument");
+    if (pt_width < 0 || pt_row_stride < pt_width)
+        return fail(MINISGL_ERR_SHAPE, "load_kv_fp4: need 0 <= pt_width <= pt_row_stride");
+    const int64_t row = (int64_t)pool->num_kv_heads * pool->head_dim;
+    if (!aligned16(k_out) || !aligned16(v_out))
+        return fail(MINISGL_ERR_SHAPE, "load_kv_fp4: k_out and v_out must be 16-byte aligned");
+    if (k_tok_stride < row || v_tok_stride < row || k_tok_stride % 8 || v_tok_stride % 8)
+        return fail(MINISGL_ERR_SHAPE, "load_kv_fp4: token strides must be >= H_kv*d and multiples of 8");
+    minisgl::LoadFp4Args a;
+    a.pool = fp4_layer(pool, layer);
+    a.page_table = page_table;
+    a.pt_stride = pt_row_stride;
+    a.pt_width = pt_width;
+    a.batch = batch;
+    a.lens = lens;
+    a.offsets = offsets;
+    a.total_tokens = total_tokens;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_tok_stride = k_tok_stride;
+    a.v_tok_stride = v_tok_stride;
+    return cuda_status(minisgl::launch_load_kv_fp4(a, static_cast<cudaStream_t>(stream)), "load_kv_fp4");
+}
+
+int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const void *q,
+                            int32_t num_q_heads, const int32_t *page_table, int32_t batch,
+                            int64_t pt_row_stride, int32_t pt_width, const int32_t *seq_lens,
+                            float sm_scale, void *out, void *workspace, size_t workspace_bytes,
+                            int32_t split_tokens, void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_decode_attn_fp4");
+    if (int rc = check_pool_fp4(pool, layer, "decode_attn_fp4")) return rc;
+    minisgl::DecodeFp4Args a;
+    if (int rc = decode_args(a.d, "decode_attn_fp4", pool->num_kv_heads, pool->head_dim, pool->num_rows, q,
+                             num_q_heads, page_table, batch, pt_row_stride, pt_width, seq_lens, sm_scale, out,
+                             workspace, workspace_bytes, split_tokens))
+        return rc;
+    if (batch == 0) return MINISGL_OK;
+    a.pool = fp4_layer(pool, layer);
+    return cuda_status(minisgl::launch_decode_fp4(a, static_cast<cudaStream_t>(stream)), "decode_attn_fp4");
 }
 
 }  // extern "C"

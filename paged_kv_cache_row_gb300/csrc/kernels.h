@@ -164,6 +164,59 @@ cudaError_t launch_check_shared_prefix(const int32_t *page_table, int32_t batch,
                                        int32_t shared_len, const int32_t *lens, uint32_t *counts,
                                        cudaStream_t s);
 
+struct SlotArgs {
+    const int32_t *cached_lens, *extend_lens;  // [batch]
+    int32_t batch;
+    int32_t *page_table;
+    int64_t pt_stride;
+    int32_t pt_width;
+    const int32_t *free_pages;    // [num_free] page numbers
+    int32_t num_free, page_size, dummy_row;
+    int32_t *out_loc, *positions; // [total_tokens]
+    int32_t *q_offsets;           // [batch + 1]
+    int32_t *seq_lens;            // [batch]
+    int32_t *pages_used;          // [1]
+    int32_t total_tokens;
+};
+cudaError_t launch_build_slots(const SlotArgs &a, cudaStream_t s);
+
+// One layer of a 4-bit pool: e2m1 pairs and e4m3 scales, strides in bytes.
+struct Fp4Layer {
+    uint8_t *k_data, *v_data, *k_scale, *v_scale;
+    int64_t data_stride, scale_stride;
+    int32_t num_rows, num_kv_heads, head_dim;
+    int32_t k_exp, v_exp;         // a value is element * scale * 2^exp
+};
+
+struct StoreFp4Args {
+    Fp4Layer pool;
+    const void *k, *v;            // bf16 rows
+    int64_t k_tok_stride, v_tok_stride;
+    const int32_t *out_loc;
+    int32_t n_tokens;
+};
+cudaError_t launch_store_kv_fp4(const StoreFp4Args &a, cudaStream_t s);
+
+struct LoadFp4Args {
+    Fp4Layer pool;
+    const int32_t *page_table;
+    int64_t pt_stride;
+    int32_t pt_width, batch;
+    const int32_t *lens, *offsets;  // [batch], [batch + 1]
+    int32_t total_tokens;
+    void *k_out, *v_out;          // bf16 rows
+    int64_t k_tok_stride, v_tok_stride;
+};
+cudaError_t launch_load_kv_fp4(const LoadFp4Args &a, cudaStream_t s);
+
+struct DecodeFp4Args {
+    DecodeArgs d;                 // k_layer, v_layer, row_stride unused
+    Fp4Layer pool;
+};
+cudaError_t launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t s);
+// The log-sum-exp merge of split partials (reads a's workspace parts).
+cudaError_t launch_decode_merge(const DecodeArgs &a, cudaStream_t s);
+
 int device_sm_count();
 
 // Sets the calling thread's minisgl_last_error() message and returns `code`.
