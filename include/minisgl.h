@@ -480,7 +480,8 @@ int minisgl_build_slots(const int32_t *cached_lens, const int32_t *extend_lens, 
  * outside the scales' range (2^-9 .. 448): -2 is a good choice where values
  * are around 1; they are powers of two so that every value the pool holds is
  * exact in bf16 (at most 6 significant bits).  data bases and strides are
- * multiples of 16 bytes, scale bases and strides multiples of head_dim/16.
+ * multiples of 16 bytes, scale bases and strides multiples of head_dim/16;
+ * row strides are below 2^31 bytes.
  */
 enum { MINISGL_FP4 = 2 };
 

@@ -716,6 +716,8 @@ int check_pool_fp4(const minisgl_kv_pool_fp4 *p, int32_t layer, const char *who)
     if (p->scale_row_stride < p->num_kv_heads * unit || p->scale_row_stride % unit)
         return fail(MINISGL_ERR_SHAPE, "%s: scale_row_stride %lld must be >= H_kv*d/16 and a multiple of d/16", who,
                     (long long)p->scale_row_stride);
+    if (p->data_row_stride > INT32_MAX || p->scale_row_stride > INT32_MAX)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: row strides must be below 2^31 bytes", who);
     if (!aligned16(p->k_data) || !aligned16(p->v_data) || p->data_layer_stride % 16)
         return fail(MINISGL_ERR_SHAPE, "%s: data bases and strides must be multiples of 16 bytes", who);
     if ((reinterpret_cast<uintptr_t>(p->k_scale) | reinterpret_cast<uintptr_t>(p->v_scale)) % unit ||

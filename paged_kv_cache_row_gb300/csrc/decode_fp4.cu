@@ -77,17 +77,24 @@ __device__ __forceinline__ int clamp_len(int n, int w) { return min(max(n, 0), w
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same with a zero accumulator.
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 // Transpose an 8x8 b16 matrix held in the mma fragment layout.
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
     return y;
 }
 
@@ -197,6 +204,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
 
     const int head_in = warp % heads, sub = warp / heads;
     const uint32_t ring = smem_u32(smem + prefix_bytes) + warp * STAGES * C::BYTES;
+    const uint32_t data_stride = (uint32_t)pool.data_stride, scale_stride = (uint32_t)pool.scale_stride;
 
     auto set_request = [&](Cursor &c) {
         c.n = clamp_len(__ldg(a.seq_lens + c.r), W);
@@ -231,21 +239,22 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
         return min(max(__ldg(a.page_table + (int64_t)c.r * a.pt_stride + tok), 0), a.num_rows - 1);
     };
     auto head_of = [&](const Cursor &c) { return c.hb * heads + head_in; };
-    auto issue = [&](int stage, const Cursor &c, int row) {
+    // one tile's rows into the ring stage at st
+    auto issue = [&](uint32_t st, const Cursor &c, int row) {
         const int head = head_of(c);
         if (head < Hkv) {
-            const uint32_t st = ring + stage * C::BYTES;
+            const int cc = lane % C::CPR;  // this lane's 16-byte chunk of every row it copies
+            const uint8_t *kd = pool.k_data + head * C::RB + cc * 16, *vd = pool.v_data + head * C::RB + cc * 16;
 #pragma unroll
             for (int i = 0; i < TILE * C::CPR / 32; ++i) {
-                const int ch = lane + 32 * i;
-                const int x = ch / C::CPR, cc = ch % C::CPR;
+                const int x = lane / C::CPR + i * (32 / C::CPR);
                 const int rr = __shfl_sync(0xffffffffu, row, x);
-                const int64_t e = (int64_t)max(rr, 0) * pool.data_stride + head * C::RB + cc * 16;
+                const uint64_t e = (uint64_t)(uint32_t)max(rr, 0) * data_stride;
                 const int bytes = rr >= 0 ? 16 : 0;
-                cp_async_16(st + x * C::RB + cc * 16, pool.k_data + e, bytes);
-                cp_async_16(st + C::V_OFF + v_chunk<D>(v_slot(x), cc), pool.v_data + e, bytes);
+                cp_async_16(st + x * C::RB + cc * 16, kd + e, bytes);
+                cp_async_16(st + C::V_OFF + v_chunk<D>(v_slot(x), cc), vd + e, bytes);
             }
-            const int64_t e = (int64_t)max(row, 0) * pool.scale_stride + head * C::SB;
+            const uint64_t e = (uint64_t)(uint32_t)max(row, 0) * scale_stride + head * C::SB;
             const int bytes = row >= 0 ? C::SB : 0;
             cp_async_small<C::SB>(st + C::KS_OFF + lane * C::SB, pool.k_scale + e, bytes);
             cp_async_small<C::SB>(st + C::VS_OFF + v_slot(lane) * C::SB, pool.v_scale + e, bytes);
@@ -262,7 +271,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
             if (t0 + s < t1) {
-                issue(s, pc, load_row(pc));
+                issue(ring + s * C::BYTES, pc, load_row(pc));
                 if (t0 + s + 1 < t1) advance(pc);
             } else {
                 cp_async_commit();
@@ -371,10 +380,11 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
                 for (int n = 0; n < NG; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
         };
 
+        uint32_t st = ring, st_in = ring + (STAGES - 1) * C::BYTES;  // stage to use, stage to fill
         for (int t = t0; t < t1; ++t) {
             const int tp = t + STAGES - 1;
             if (tp < t1) {
-                issue((tp - t0) % STAGES, pc, row_next);
+                issue(st_in, pc, row_next);
                 if (tp + 1 < t1) {
                     advance(pc);
                     row_next = load_row(pc);
@@ -394,13 +404,10 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
             cp_async_wait<STAGES - 1>();
             __syncwarp();
 
-            const uint32_t st = ring + ((t - t0) % STAGES) * C::BYTES;
             // ---- S^T = K Q^T for two blocks of 16 tokens ----
             float sa[2][NG][4];
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-#pragma unroll
-                for (int n = 0; n < NG; ++n) sa[b][n][0] = sa[b][n][1] = sa[b][n][2] = sa[b][n][3] = 0.f;
                 constexpr int WORDS = C::QPT / 8;  // 32-bit words of a lane's channels
                 uint32_t k0[WORDS], k1[WORDS];
                 const int x0 = 16 * b + lg, x1 = x0 + 8;
@@ -432,7 +439,10 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
                     }
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
-                        mma_f16_16816(sa[b][n], e0[0], e1[0], e0[1], e1[1], qb[n][2 * i][0], qb[n][2 * i][1]);
+                        if (i == 0)
+                            mma_f16_16816_first(sa[b][n], e0[0], e1[0], e0[1], e1[1], qb[n][0][0], qb[n][0][1]);
+                        else
+                            mma_f16_16816(sa[b][n], e0[0], e1[0], e0[1], e1[1], qb[n][2 * i][0], qb[n][2 * i][1]);
                         mma_f16_16816(sa[b][n], e0[2], e1[2], e0[3], e1[3], qb[n][2 * i + 1][0], qb[n][2 * i + 1][1]);
                     }
                 }
@@ -441,32 +451,35 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
             uint32_t pb[2][NG][2];
 #pragma unroll
             for (int n = 0; n < NG; ++n) {
-                float x[2][4];  // [e][token]
+                float x[2][4];  // [e][token]: scores less the reference, then weights
+                auto scores = [&]() {
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                    for (int e = 0; e < 2; ++e)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[e][i] = sa[i >> 1][n][2 * (i & 1) + e] * sc[n][e];
-                if (cc.j == cc.nt - 1) {
+                        for (int i = 0; i < 4; ++i)
+                            x[e][i] = fmaf(sa[i >> 1][n][2 * (i & 1) + e], sc[n][e], -ref[n][e]);
+                    if (cc.j == cc.nt - 1) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (cc.j * TILE + lg + 8 * i >= cc.n) x[0][i] = x[1][i] = -INFINITY;
-                }
+                        for (int i = 0; i < 4; ++i)
+                            if (cc.j * TILE + lg + 8 * i >= cc.n) x[0][i] = x[1][i] = -INFINITY;
+                    }
+                };
+                scores();
                 float mx[2];
-                bool over = false;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
-                    over |= mx[e] > ref[n][e] + REF_ROOM;
-                }
-                if (__any_sync(0xffffffffu, over)) {
+                for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
+                if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > REF_ROOM)) {
+                    const float old[2] = {ref[n][0], ref[n][1]};
+                    ref[n][0] = ref[n][1] = 0.f;
+                    scores();  // the scores themselves: the first reference is too far off to add back
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
+                        mx[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 8));
                         mx[e] = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 16));
-                        const float to = fmaxf(ref[n][e], mx[e] - REF_BELOW);
-                        const float al = ex2(ref[n][e] - to);
-                        ref[n][e] = to;
+                        ref[n][e] = fmaxf(old[e], mx[e] - REF_BELOW);
+                        const float al = ex2(old[e] - ref[n][e]);
                         l[n][e] *= al;
 #pragma unroll
                         for (int mt = 0; mt < C::MT; ++mt) {
@@ -474,12 +487,13 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
                             o[mt][n][2 + e] *= al;
                         }
                     }
+                    scores();
                 }
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[e][i] = ex2(x[e][i] - ref[n][e]);
+                        x[e][i] = ex2(x[e][i]);
                         l[n][e] += x[e][i];
                     }
                 // P^T as the B operand: transpose the 8x8 token-by-head blocks
@@ -520,6 +534,8 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, NG == 1 ? 2 : 1)
             }
             last_j = cc.j;
             if (t + 1 < t1) advance(cc);
+            st_in = st;
+            st = st == ring + (STAGES - 1) * C::BYTES ? ring : st + C::BYTES;
             __syncwarp();
         }
         if (cur_r >= 0) flush();
