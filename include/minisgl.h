@@ -567,9 +567,10 @@ int32_t minisgl_device_sm_count(void);
  * threads. */
 int minisgl_debug_set_pdl(int enabled);
 
-/* Debugging aid: how many bounded waits inside the tensor-core kernels ran
- * out of time since the library was loaded on the current device.  A
- * non-zero count means some minisgl_extend_attn output is garbage.  This call
+/* Debugging aid: how many bounded waits inside the tensor-core kernels and
+ * the 4-bit decode kernel ran out of time since the library was loaded on
+ * the current device.  A non-zero count means some minisgl_extend_attn or
+ * minisgl_decode_attn_fp4 output is garbage.  This call
  * synchronises with the device (it reads a device counter), so it is not
  * for the hot path. */
 int minisgl_debug_timeout_count(uint32_t *count);

@@ -811,7 +811,7 @@ def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, l
     return k_out, v_out
 
 
-def decode_workspace_fp4(batch: int, num_q_heads: int, pool: KVPoolFP4, max_splits: int = 16) -> torch.Tensor:
+def decode_workspace_fp4(batch: int, num_q_heads: int, pool: KVPoolFP4, max_splits: int = 32) -> torch.Tensor:
     """A new workspace for minisgl_decode_attn_fp4 on the pool's device.  Calls
     that may run at the same time need different ones."""
     return torch.empty(minisgl_decode_workspace_bytes(batch, num_q_heads, pool.num_kv_heads, pool.head_dim,
@@ -821,7 +821,7 @@ def decode_workspace_fp4(batch: int, num_q_heads: int, pool: KVPoolFP4, max_spli
 def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_table: torch.Tensor,
                             seq_lens: torch.Tensor, sm_scale: float, out: Optional[torch.Tensor] = None,
                             workspace: Optional[torch.Tensor] = None, split_tokens: int = 0,
-                            max_splits: int = 16, stream=None) -> torch.Tensor:
+                            max_splits: int = 32, stream=None) -> torch.Tensor:
     """Decode attention of q [B, H_q, d] over each request's page_table row of
     the 4-bit pool.  Without a workspace the call allocates its own."""
     lib = load_library()

@@ -134,8 +134,10 @@ int minisgl_debug_timeout_count(uint32_t *count) {
     g_err.clear();
     if (!count) return fail(MINISGL_ERR_ARG, "debug_timeout_count: NULL count");
     unsigned int c = 0;
+    unsigned int d = 0;
     if (int rc = cuda_status(minisgl::read_kernel_timeouts(&c), "debug_timeout_count")) return rc;
-    *count = c;
+    if (int rc = cuda_status(minisgl::read_fp4_timeouts(&d), "debug_timeout_count")) return rc;
+    *count = c + d;
     return MINISGL_OK;
 }
 

@@ -225,5 +225,7 @@ int report_error(int code, const char *msg);
 // Number of bounded waits that ran out in tensor-core kernels since load
 // (synchronous copy from a device counter).
 cudaError_t read_kernel_timeouts(unsigned int *count);
+// The same for the 4-bit decode kernel.
+cudaError_t read_fp4_timeouts(unsigned int *count);
 
 }  // namespace minisgl
