@@ -68,7 +68,7 @@ __host__ __device__ constexpr int record_stride(int heads) {
 // Bounded wait: once one wait has run out, the CTA stops waiting altogether,
 // so every warp reaches the end (the output is then garbage and counted).
 __device__ __forceinline__ void guarded_wait(uint32_t b, uint32_t parity, volatile int *abort_flag) {
-    if (mbar_test_wait(b, parity)) return;
+    if (mbar_try_wait(b, parity)) return;
     if (*abort_flag) return;
     if (!mbar_wait(b, parity, WAIT_LIMIT)) {
         *abort_flag = 1;
@@ -87,8 +87,9 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 
 }  // namespace
 
-// HEADS: lay.heads when it is known here (8: the record stride becomes a
-// constant and its multiples offsets of the load instructions), else 0.
+// HEADS: 8 when there are 8 KV heads and their scales are 16-byte pieces (the
+// record stride is a constant then, and a warp's share of a tile 4 tokens in
+// 9 copies at d 128), else 0.
 template <int D, int NG, int HEADS>
 __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     decode_fp4_kernel(const DecodeFp4Args args, const float scale_log2, const float out_scale, const Layout lay) {
@@ -125,10 +126,11 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
 
     // This warp fetches tokens head_in + heads * i of a tile, i < mine; lane i
     // holds the i-th one's physical row (past the end: the last token's).
-    const int mine = HEADS && TILE % HEADS == 0 ? TILE / heads : (TILE - head_in + heads - 1) / heads;
-    auto load_row = [&](const Cursor &c) -> int {
-        const int tok = min(c.j * TILE + min(head_in + heads * lane, TILE - 1), c.n - 1);
-        return min(max(__ldg(a.page_table + (int64_t)c.r * a.pt_stride + tok), 0), a.num_rows - 1);
+    const int mine = HEADS ? TILE / 8 : (TILE - head_in + heads - 1) / heads;
+    const int my_tok = min(head_in + heads * lane, TILE - 1);
+    const int32_t *table = nullptr;  // entry of the first token of the tile to fetch
+    auto load_row = [&](int left) -> int {
+        return min(max(__ldg(table + min(my_tok, left - 1)), 0), a.num_rows - 1);
     };
     // The pieces of a token's K and V rows are dealt to lanes in powers of two:
     // 2^lp >= pieces lanes to a token (or all 32, several times), and the same
@@ -136,34 +138,34 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     const int pieces = 2 * heads * C::RB / 16, half = pieces / 2;
     const int lp = pieces >= 32 ? 5 : 32 - __clz(pieces - 1), times = (pieces + 31) / 32;
     const int spieces = 2 * heads * C::SB / lay.scale_bytes, shalf = spieces / 2;
-    const int slp = 32 - __clz(spieces - 1);
+    const int slp = HEADS ? (D == 128 ? 3 : 2) : 32 - __clz(spieces - 1);
     const int sub_tok = lane >> lp, piece0 = lane & ((1 << lp) - 1);
     const int ssub_tok = lane >> slp, spiece = lane & ((1 << slp) - 1);
     const bool s_isv = spiece >= shalf;
     const int soff = (s_isv ? spiece - shalf : spiece) * lay.scale_bytes;
     const uint8_t *const ssrc = (s_isv ? pool.v_scale : pool.k_scale) + soff;
     const uint32_t sdst = sk_off + spiece * lay.scale_bytes;
+    // 8 heads: this lane's piece of K (or, at d 64, of K or V), and where its pieces go
+    const uint8_t *const ksrc = (D == 64 && lane >= 16 ? pool.v_data - 256 : pool.k_data) + lane * 16;
+    const uint8_t *const vsrc = pool.v_data + lane * 16;
+    const uint32_t kto = fp4::slot(head_in) * stride + lane * 16;
+    const uint32_t sto = fp4::slot(head_in + 8 * ssub_tok) * stride + sdst;
 
-    int in_stage = 0, in_parity = 1;  // the first round finds every stage empty
-    auto issue = [&](const Cursor &c, int row) {
-        const int h0 = c.hb * heads, nh = min(heads, Hkv - h0);
-        const uint32_t bar = bars + in_stage * 16u, dst = ring + in_stage * stage_bytes;
+    uint32_t in_at = 0, in_parity = 1;  // stage to fill; the first round finds every stage empty
+    auto issue = [&](int hb, int row) {
+        const uint32_t bar = bars + in_at * 16u, dst = ring + in_at * stage_bytes;
         guarded_wait(bar + 8u, in_parity, &s_abort);
-        if constexpr (HEADS == 8) {  // one head block; token slots 8 apart
-            const uint32_t to = dst + fp4::slot(head_in) * stride + piece0 * 16;
-            const uint8_t *kd = pool.k_data + h0 * C::RB, *vd = pool.v_data + h0 * C::RB;
+        if constexpr (HEADS == 8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int rr = __shfl_sync(0xffffffffu, row, i);
-                const uint64_t e = (uint64_t)(uint32_t)rr * data_stride;
-                if constexpr (D == 128) {
-                    cp_async_16(to + 8 * i * stride, kd + lane * 16 + e, 16);
-                    cp_async_16(to + 8 * i * stride + 512, vd + lane * 16 + e, 16);
-                } else {
-                    cp_async_16(to + 8 * i * stride, (lane < 16 ? kd + lane * 16 : vd + (lane - 16) * 16) + e, 16);
-                }
+            for (int i = 0; i < TILE / 8; ++i) {
+                const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i) * data_stride;
+                cp_async_16(dst + kto + 8 * i * stride, ksrc + e, 16);
+                if constexpr (D == 128) cp_async_16(dst + kto + 8 * i * stride + 8 * C::RB, vsrc + e, 16);
             }
+            const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, ssub_tok) * scale_stride;
+            if (D == 128 || lane < 16) cp_async_16(dst + sto, ssrc + e, 16);
         } else {
+            const int h0 = hb * heads, nh = min(heads, Hkv - h0);
             for (int i0 = 0; i0 < mine; i0 += 1 << (5 - lp)) {
                 const int i = i0 + sub_tok;
                 const int rr = __shfl_sync(0xffffffffu, row, i);
@@ -177,75 +179,90 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
                         cp_async_16(to + piece * 16, (isv ? pool.v_data : pool.k_data) + e + off, 16);
                 }
             }
-        }
-        for (int i0 = 0; i0 < mine; i0 += 1 << (5 - slp)) {
-            const int i = i0 + ssub_tok;
-            const int rr = __shfl_sync(0xffffffffu, row, i);
-            const uint8_t *src = ssrc + (uint64_t)(uint32_t)rr * scale_stride + h0 * C::SB;
-            const uint32_t to = dst + fp4::slot(head_in + heads * i) * stride + sdst;
-            if (i < mine && spiece < spieces && soff < nh * C::SB) {
-                if (lay.scale_bytes == 16) cp_async_16(to, src, 16);
-                else cp_async_small<C::SB>(to, src);
+            for (int i0 = 0; i0 < mine; i0 += 1 << (5 - slp)) {
+                const int i = i0 + ssub_tok;
+                const int rr = __shfl_sync(0xffffffffu, row, i);
+                const uint8_t *src = ssrc + (uint64_t)(uint32_t)rr * scale_stride + h0 * C::SB;
+                const uint32_t to = dst + fp4::slot(head_in + heads * i) * stride + sdst;
+                if (i < mine && spiece < spieces && soff < nh * C::SB) {
+                    if (lay.scale_bytes == 16) cp_async_16(to, src, 16);
+                    else cp_async_small<C::SB>(to, src);
+                }
             }
         }
         cp_async_arrive(bar);
-        if (++in_stage == stages) {
-            in_stage = 0;
+        if (++in_at == (uint32_t)stages) {
+            in_at = 0;
             in_parity ^= 1;
         }
     };
 
     fp4::Stream<D, NG> w;
-    int stage = 0, parity = 0;
+    uint32_t at = 0, parity = 0;  // stage to use
+    const uint32_t my_k = ring + head_in * C::RB, my_s = ring + sk_off + head_in * C::SB;
     const int64_t seg_step = (int64_t)gridDim.x * lay.subs;
     for (int64_t seg = (int64_t)blockIdx.x * lay.subs + sub; seg < sch.nseg; seg += seg_step) {
         const int t0 = sch.begin(seg), t1 = sch.begin(seg + 1);
         Cursor c, pc;  // the tile to use, the tile to fetch
         sch.locate(c, t0);
         pc = c;
-        int tp = t0;
-        for (; tp < t1 && tp < t0 + stages - 1; ++tp) {
-            issue(pc, load_row(pc));
-            if (tp + 1 < t1) sch.advance(pc);
+        auto set_table = [&]() { table = a.page_table + (int64_t)pc.r * a.pt_stride + (sch.len(pc.r) - pc.left); };
+        auto fetch_next = [&]() {  // only called when a next tile exists
+            pc.left -= TILE;
+            table += TILE;
+            if (pc.left <= 0) {
+                sch.next_stream(pc);
+                set_table();
+            }
+        };
+        set_table();
+        int todo = t1 - t0;  // tiles not asked for yet
+        for (int i = 0; i < stages - 1 && todo > 0; ++i) {
+            issue(pc.hb, load_row(pc.left));
+            if (--todo > 0) fetch_next();
         }
         int row = 0;
-        if (tp < t1) row = load_row(pc);
-        int first_j = c.j;
+        if (todo > 0) row = load_row(pc.left);
+        bool open = true, from_start = c.left == sch.len(c.r);
         for (int t = t0; t < t1; ++t) {
-            const int head = c.hb * heads + head_in;
-            const bool live = head < Hkv;
-            const int64_t row0 = (int64_t)c.r * Hq + head * G;
-            if (t == t0 || c.j == 0) {
-                first_j = c.j;
-                w.open(live ? static_cast<const __nv_bfloat16 *>(a.q) + row0 * D : nullptr, G, scale_log2, lane);
+            const int head = HEADS ? head_in : c.hb * heads + head_in;
+            const bool live = HEADS || head < Hkv;
+            if (open) {
+                open = false;
+                w.open(live ? static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)c.r * Hq + head * G) * D : nullptr, G,
+                       scale_log2, lane);
             }
-            guarded_wait(bars + stage * 16u, parity, &s_abort);
+            guarded_wait(bars + at * 16u, parity, &s_abort);
             if (live) {
-                const uint32_t st = ring + stage * stage_bytes;
-                w.add(st + head_in * C::RB, st + v_off + head_in * C::RB, st + sk_off + head_in * C::SB,
-                      st + sv_off + head_in * C::SB, stride, c.n - c.j * TILE, lane);
+                const uint32_t st = at * stage_bytes;
+                w.add(my_k + st, my_k + st + v_off, my_s + st, my_s + st + (sv_off - sk_off), stride, c.left, lane);
             }
-            if (tp < t1) {
-                issue(pc, row);  // into the stage of tile t - 1
-                if (++tp < t1) {
-                    sch.advance(pc);
-                    row = load_row(pc);  // for the next iteration
+            if (todo > 0) {
+                issue(pc.hb, row);  // into the stage of the tile before this one
+                if (--todo > 0) {
+                    fetch_next();
+                    row = load_row(pc.left);  // for the next iteration
                 }
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars + stage * 16u + 8u);
-            if (++stage == stages) {
-                stage = 0;
+            if (lane == 0) mbar_arrive(bars + at * 16u + 8u);
+            if (++at == (uint32_t)stages) {
+                at = 0;
                 parity ^= 1;
             }
-            const bool last = c.j == c.nt - 1;
-            if (live && (last || t + 1 == t1)) {
-                const bool whole = first_j == 0 && last;
-                const int split = whole ? 0 : (int)(seg - sch.range_of(sch.first_tile(c)));
-                w.close(a, row0, G, whole, split, out_scale, lane);
-                if (last && lane == 0) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
+            c.left -= TILE;
+            if (c.left <= 0 || t + 1 == t1) {  // end of the stream or of the range
+                const bool last = c.left <= 0;
+                if (live) {
+                    const bool whole = from_start && last;
+                    const int nt = (sch.len(c.r) + TILE - 1) / TILE;
+                    const int split = whole ? 0 : (int)(seg - sch.range_of(sch.prefix[c.r] + c.hb * nt));
+                    w.close(a, (int64_t)c.r * Hq + head * G, G, whole, split, out_scale, lane);
+                    if (last && lane == 0) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
+                }
+                if (t + 1 < t1) sch.next_stream(c);
+                open = from_start = true;
             }
-            if (t + 1 < t1) sch.advance(c);
         }
     }
     cp_async_wait<0>();  // nothing in flight when the CTA ends, even after a wait that ran out
@@ -325,7 +342,10 @@ cudaError_t launch_heads(const DecodeFp4Args &a, cudaStream_t s) {
     constexpr int most = MAX_WARPS<D, NG>;
     lay.hblocks = (a.d.num_kv_heads + most - 1) / most;
     lay.heads = (a.d.num_kv_heads + lay.hblocks - 1) / lay.hblocks;
-    return lay.heads * lay.hblocks == a.d.num_kv_heads && lay.heads == 8 ? launch_cfg<D, NG, 8>(a, lay, s) : launch_cfg<D, NG, 0>(a, lay, s);
+    const Fp4Layer &p = a.pool;
+    const bool wide = p.scale_stride % 16 == 0 &&
+                      ((reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) & 15u) == 0;
+    return p.num_kv_heads == 8 && wide ? launch_cfg<D, NG, 8>(a, lay, s) : launch_cfg<D, NG, 0>(a, lay, s);
 }
 
 }  // namespace

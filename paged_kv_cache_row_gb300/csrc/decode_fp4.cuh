@@ -345,8 +345,10 @@ struct Stream {
 // ---- the cut of the work into ranges ---------------------------------------
 constexpr int TILE = 32;  // tokens of a tile
 
+// A tile: its request and head block, and the tokens from its first one to
+// the end of the request's context.
 struct Cursor {
-    int r, hb, j, nt, n;  // request, head block, tile in stream, tiles in stream, tokens
+    int r, hb, left;
 };
 
 // Every CTA derives the same schedule from seq_lens: the tiles of all streams
@@ -401,33 +403,26 @@ struct Schedule {
     __device__ __forceinline__ int begin(int64_t seg) const { return (int)(seg * total / nseg); }
     // the range that holds tile t
     __device__ __forceinline__ int64_t range_of(int t) const { return (((int64_t)t + 1) * nseg - 1) / total; }
-    __device__ __forceinline__ void set_request(Cursor &c) const {
-        c.n = clamp_len(__ldg(seq_lens + c.r), W);
-        c.nt = (c.n + TILE - 1) / TILE;
-    }
+    __device__ __forceinline__ int len(int r) const { return clamp_len(__ldg(seq_lens + r), W); }
     __device__ __forceinline__ void locate(Cursor &c, int t) const {
         int lo = 0, hi = B;  // largest r with prefix[r] <= t
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (prefix[mid] <= t) lo = mid; else hi = mid;
         }
+        const int n = len(lo), nt = (n + TILE - 1) / TILE, off = t - prefix[lo];
         c.r = lo;
-        set_request(c);
-        const int off = t - prefix[lo];
-        c.hb = off / c.nt;
-        c.j = off - c.hb * c.nt;
+        c.hb = off / nt;
+        c.left = n - (off - c.hb * nt) * TILE;
     }
-    __device__ __forceinline__ void advance(Cursor &c) const {  // only called when a next tile exists
-        if (++c.j == c.nt) {
-            c.j = 0;
-            if (++c.hb == hblocks) {
-                c.hb = 0;
-                do { ++c.r; } while (prefix[c.r + 1] == prefix[c.r]);
-                set_request(c);
-            }
+    // To the first tile of the next stream (there is one).
+    __device__ __forceinline__ void next_stream(Cursor &c) const {
+        if (++c.hb == hblocks) {
+            c.hb = 0;
+            do { ++c.r; } while (prefix[c.r + 1] == prefix[c.r]);
         }
+        c.left = len(c.r);
     }
-    __device__ __forceinline__ int first_tile(const Cursor &c) const { return prefix[c.r] + c.hb * c.nt; }
 };
 
 }  // namespace fp4
