@@ -21,10 +21,15 @@
 // each.  The group's warps fetch a tile together, each its share of the
 // tokens, in 16-byte cp.async pieces: a warp instruction covers a token's K
 // row of eight heads (512 bytes at d 128), so few rows and lines are touched
-// at a time.  (Every warp fetching its own head's 64- and 8-byte pieces took
-// 241 us where this takes XX, and one bulk copy (TMA) per row 396: about 41
-// cycles a copy and SM, whatever its size.)  Rows past a request's end repeat
-// its last row; their weights are zero.
+// at a time.  Page-table entries are read a tile before the rows they name.
+// Rows past a request's end repeat its last row; their weights are zero.
+//
+// Arrangements timed and not kept, 256 requests of 1k to 8k tokens (8 KV
+// heads, d 128; this one takes 156 us): every warp fetching its own head's
+// 64- and 8-byte pieces 241; one barrier per tile instead of the mbarriers
+// 204 (174 then); one bulk copy (TMA) per row 396, about 41 cycles a copy and
+// SM, whatever its size; four producer warps, eight consumers and six stages
+// 164.
 #include <cmath>
 #include <mutex>
 
@@ -130,7 +135,7 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     const int my_tok = min(head_in + heads * lane, TILE - 1);
     const int32_t *table = nullptr;  // entry of the first token of the tile to fetch
     auto load_row = [&](int left) -> int {
-        return min(max(__ldg(table + min(my_tok, left - 1)), 0), a.num_rows - 1);
+        return __ldg(table + min(my_tok, left - 1));
     };
     // The pieces of a token's K and V rows are dealt to lanes in powers of two:
     // 2^lp >= pieces lanes to a token (or all 32, several times), and the same
@@ -152,7 +157,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     const uint32_t sto = fp4::slot(head_in + 8 * ssub_tok) * stride + sdst;
 
     uint32_t in_at = 0, in_parity = 1;  // stage to fill; the first round finds every stage empty
-    auto issue = [&](int hb, int row) {
+    auto issue = [&](int hb, int raw) {
+        const int row = min(max(raw, 0), a.num_rows - 1);
         const uint32_t bar = bars + in_at * 16u, dst = ring + in_at * stage_bytes;
         guarded_wait(bar + 8u, in_parity, &s_abort);
         if constexpr (HEADS == 8) {
@@ -233,9 +239,11 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
                        scale_log2, lane);
             }
             guarded_wait(bars + at * 16u, parity, &s_abort);
+            const uint32_t st = at * stage_bytes;
+            uint32_t pb[2][NG][2];
             if (live) {
-                const uint32_t st = at * stage_bytes;
-                w.add(my_k + st, my_k + st + v_off, my_s + st, my_s + st + (sv_off - sk_off), stride, c.left, lane);
+                w.scores(my_k + st, my_s + st, stride, c.left, lane, pb);
+                w.values(my_k + st + v_off, my_s + st + (sv_off - sk_off), stride, lane, pb);
             }
             if (todo > 0) {
                 issue(pc.hb, row);  // into the stage of the tile before this one
@@ -255,8 +263,7 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
                 const bool last = c.left <= 0;
                 if (live) {
                     const bool whole = from_start && last;
-                    const int nt = (sch.len(c.r) + TILE - 1) / TILE;
-                    const int split = whole ? 0 : (int)(seg - sch.range_of(sch.prefix[c.r] + c.hb * nt));
+                    const int split = whole ? 0 : (int)(seg - sch.range_of(sch.before(c.r, c.hb)));
                     w.close(a, (int64_t)c.r * Hq + head * G, G, whole, split, out_scale, lane);
                     if (last && lane == 0) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
                 }
@@ -314,7 +321,7 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, Layout lay, cudaStream_t s) {
     const bool wide = sb % 16 == 0 && sb_last % 16 == 0 && p.scale_stride % 16 == 0 &&
                       ((reinterpret_cast<uintptr_t>(p.k_scale) | reinterpret_cast<uintptr_t>(p.v_scale)) & 15u) == 0;
     lay.scale_bytes = wide ? 16 : C::SB;
-    lay.off_bars = align_up((a.batch + 2) * 4, 16);
+    lay.off_bars = align_up(fp4::schedule_ints(a.batch) * 4, 16);
     lay.off_ring = align_up(lay.off_bars + MAX_STAGES * lay.subs * 16, 128);
     auto kern = decode_fp4_kernel<D, NG, HEADS>;
     int optin = 0;

@@ -165,10 +165,11 @@ struct Stream {
             for (int n = 0; n < NG; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
 
-    // Adds 32 tokens, the first `left` of which count.  k, v, sk, sv: shared
-    // addresses of this head's K row, V row, K scales and V scales in slot 0.
-    __device__ __forceinline__ void add(uint32_t k, uint32_t v, uint32_t sk, uint32_t sv, int stride, int left,
-                                        int lane) {
+    // The weights of 32 tokens, the first `left` of which count, as the B
+    // operand of the product with V.  k, sk: shared addresses of this head's K
+    // row and K scales in slot 0.
+    __device__ __forceinline__ void scores(uint32_t k, uint32_t sk, int stride, int left, int lane,
+                                           uint32_t (&pb)[2][NG][2]) {
         const int lg = lane >> 2, lt = lane & 3;
         // ---- S^T = K Q^T for two blocks of 16 tokens ----
         float sa[2][NG][4];
@@ -214,11 +215,10 @@ struct Stream {
             }
         }
         // ---- softmax weights; this lane holds tokens lg + 8*i (i < 4) ----
-        uint32_t pb[2][NG][2];
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
             float x[2][4];  // [e][token]: scores less the reference, then weights
-            auto scores = [&]() {
+            auto relative = [&]() {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -230,14 +230,14 @@ struct Stream {
                         if (lg + 8 * i >= left) x[0][i] = x[1][i] = -INFINITY;
                 }
             };
-            scores();
+            relative();
             float mx[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
             if (__any_sync(0xffffffffu, fmaxf(mx[0], mx[1]) > REF_ROOM)) {
                 const float old[2] = {ref[n][0], ref[n][1]};
                 ref[n][0] = ref[n][1] = 0.f;
-                scores();  // the scores themselves: the first reference is too far off to add back
+                relative();  // the scores themselves: the first reference is too far off to add back
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     mx[e] = fmaxf(fmaxf(x[e][0], x[e][1]), fmaxf(x[e][2], x[e][3]));
@@ -253,7 +253,7 @@ struct Stream {
                         o[mt][n][2 + e] *= al;
                     }
                 }
-                scores();
+                relative();
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -266,7 +266,12 @@ struct Stream {
 #pragma unroll
             for (int i = 0; i < 4; ++i) pb[i >> 1][n][i & 1] = movmatrix_t(f32_to_f16x2(x[0][i], x[1][i]));
         }
-        // ---- O^T += V^T P^T ----
+    }
+
+    // O^T += V^T P^T for the same tokens; v, sv: this head's V row and V scales in slot 0.
+    __device__ __forceinline__ void values(uint32_t v, uint32_t sv, int stride, int lane,
+                                           const uint32_t (&pb)[2][NG][2]) {
+        const int lg = lane >> 2, lt = lane & 3;
         // tokens 2lt, 2lt+1, 2lt+8, 2lt+9 of a block: slots lt, 4 + (lt ^ 2), and 8 more
         const uint32_t vo = lg * (C::OPT / 2), so = D == 128 ? lg : lg >> 1;
         const uint32_t vp[2] = {v + lt * stride + vo, v + (4 + (lt ^ 2)) * stride + vo};
@@ -353,50 +358,72 @@ struct Cursor {
 
 // Every CTA derives the same schedule from seq_lens: the tiles of all streams
 // (request, head block) in a row, cut into nseg ranges whose lengths differ
-// by at most one tile.
+// by at most one tile.  The prefix sums are kept for every CHUNK-th request
+// only, so that they leave room for the rings at the largest batch.
+constexpr int CHUNK = 4;
+__host__ __device__ constexpr int schedule_ints(int batch) { return (batch + CHUNK - 1) / CHUNK + 2; }
+
 struct Schedule {
-    const int32_t *prefix;  // shared, [B + 1]: tiles before each request
+    const int32_t *prefix;  // shared: tiles before request CHUNK * k, then all tiles
     const int32_t *seq_lens;
-    int B, W, hblocks, total;
+    int W, hblocks, chunks, total;
     int64_t nseg;
 
-    // Called by all threads of the CTA; prefix has room for B + 2 ints.
+    // Called by all threads of the CTA; s_prefix has room for schedule_ints(batch).
     __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int64_t ranges) {
         prefix = s_prefix;
         seq_lens = a.seq_lens;
-        B = a.batch;
         W = a.pt_width;
         hblocks = hblocks_;
-        const int lane = threadIdx.x & 31;
-        if (threadIdx.x < 32) {
-            int carry = 0, mx = 0;
-            if (lane == 0) s_prefix[0] = 0;
-            for (int base = 0; base < B; base += 32) {
-                const int r = base + lane;
-                int nt = 0;
-                if (r < B) nt = (clamp_len(__ldg(seq_lens + r), W) + TILE - 1) / TILE;
-                mx = max(mx, nt);
-                int v = nt * hblocks;
+        chunks = (a.batch + CHUNK - 1) / CHUNK;
+        // every thread sums the tiles of its chunks, then a scan over the CTA
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+        __shared__ int s_sum[32], s_max[32];
+        const int each = (chunks + blockDim.x - 1) / blockDim.x;
+        const int k0 = min(tid * each, chunks), k1 = min(k0 + each, chunks);
+        int mine = 0, mx = 0;
+        for (int r = k0 * CHUNK; r < min(k1 * CHUNK, a.batch); ++r) {
+            const int nt = tiles(r);
+            mine += nt;
+            mx = max(mx, nt);
+        }
+        mine *= hblocks;
+        int inc = mine;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int u = __shfl_up_sync(0xffffffffu, v, o);
-                    if (lane >= o) v += u;
-                }
-                if (r < B) s_prefix[r + 1] = carry + v;
-                carry += __shfl_sync(0xffffffffu, v, 31);
-            }
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
 #pragma unroll
-            for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (lane == 0) s_prefix[B + 1] = mx;
+        for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (lane == 31) {
+            s_sum[warp] = inc;
+            s_max[warp] = mx;
         }
         __syncthreads();
-        total = s_prefix[B];
+        int at = inc - mine;  // tiles before this thread's chunks
+        for (int w = 0; w < warp; ++w) at += s_sum[w];
+        for (int k = k0; k < k1; ++k) {
+            s_prefix[k] = at;
+            for (int r = k * CHUNK; each > 1 && r < min((k + 1) * CHUNK, a.batch); ++r) at += tiles(r) * hblocks;
+        }
+        if (tid == 0) {
+            int all = 0, longest = 0;
+            for (int w = 0; w < warps; ++w) {
+                all += s_sum[w];
+                longest = max(longest, s_max[w]);
+            }
+            s_prefix[chunks] = all;
+            s_prefix[chunks + 1] = longest;
+        }
+        __syncthreads();
+        total = s_prefix[chunks];
         // Ranges [seg * total / nseg, (seg + 1) * total / nseg), each at least
         // L = total / nseg >= 1 tiles long.  A stream of nt tiles meets at most
         // (nt - 2) / L + 2 of them, and L >= (nt - 1) / (max_splits - 1) keeps
         // that within max_splits.
         int want = a.split_tokens > 0 ? (int)(((int64_t)a.split_tokens + TILE - 1) / TILE) : 1;
-        want = max(want, (s_prefix[B + 1] + a.max_splits - 2) / (a.max_splits - 1));
+        want = max(want, (s_prefix[chunks + 1] + a.max_splits - 2) / (a.max_splits - 1));
         if (a.split_tokens > 0) ranges = total / want;
         nseg = max((int64_t)1, min(ranges, (int64_t)(total / want)));
     }
@@ -404,22 +431,34 @@ struct Schedule {
     // the range that holds tile t
     __device__ __forceinline__ int64_t range_of(int t) const { return (((int64_t)t + 1) * nseg - 1) / total; }
     __device__ __forceinline__ int len(int r) const { return clamp_len(__ldg(seq_lens + r), W); }
+    __device__ __forceinline__ int tiles(int r) const { return (len(r) + TILE - 1) / TILE; }
+    // tiles before head block hb of request r
+    __device__ __forceinline__ int before(int r, int hb) const {
+        int t = prefix[r / CHUNK] + hb * tiles(r);
+        for (int q = r - r % CHUNK; q < r; ++q) t += tiles(q) * hblocks;
+        return t;
+    }
     __device__ __forceinline__ void locate(Cursor &c, int t) const {
-        int lo = 0, hi = B;  // largest r with prefix[r] <= t
+        int lo = 0, hi = chunks;  // largest chunk with prefix <= t: it holds tile t
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (prefix[mid] <= t) lo = mid; else hi = mid;
         }
-        const int n = len(lo), nt = (n + TILE - 1) / TILE, off = t - prefix[lo];
-        c.r = lo;
+        int off = t - prefix[lo];
+        c.r = lo * CHUNK;
+        int nt = tiles(c.r);
+        while (off >= nt * hblocks) {
+            off -= nt * hblocks;
+            nt = tiles(++c.r);
+        }
         c.hb = off / nt;
-        c.left = n - (off - c.hb * nt) * TILE;
+        c.left = len(c.r) - (off - c.hb * nt) * TILE;
     }
     // To the first tile of the next stream (there is one).
     __device__ __forceinline__ void next_stream(Cursor &c) const {
         if (++c.hb == hblocks) {
             c.hb = 0;
-            do { ++c.r; } while (prefix[c.r + 1] == prefix[c.r]);
+            do { ++c.r; } while (len(c.r) == 0);
         }
         c.left = len(c.r);
     }
