@@ -594,30 +594,28 @@ def minisgl_check_shared_prefix(page_table: torch.Tensor, lens: torch.Tensor, sh
 FP4_BLOCK = 16  # channels that share a scale
 
 
+# The current stream's handle for a device index (torch.cuda.current_stream
+# builds a Stream object first, which takes longer than a kernel launch).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 class _On:
-    """The stream a call runs on, with the tensors' device (and a stream that
-    the caller named) made current for the call's own allocations and launches."""
+    """The stream a call runs on, with its device (and a stream that the caller
+    named) current for the call's own allocations and launches."""
     __slots__ = ("handle", "_ctx")
 
-    def __init__(self, stream, *tensors: Optional[torch.Tensor]):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise MinisglError(f"tensors on different devices: {dev} and {t.device}")
+    def __init__(self, stream, index: int):
         self._ctx = None
         if stream is None:
-            stream = torch.cuda.current_stream(dev)
-            if torch.cuda.current_device() != dev.index:
-                self._ctx = torch.cuda.device(dev)
+            self.handle = _raw_stream(index)
+            if torch.cuda.current_device() != index:
+                self._ctx = torch.cuda.device(index)
         else:
-            if stream.device != dev:
-                raise MinisglError(f"stream on {stream.device}, tensors on {dev}")
+            if stream.device.index != index:
+                raise MinisglError(f"stream on {stream.device}, tensors on cuda:{index}")
+            self.handle = stream.cuda_stream
             self._ctx = torch.cuda.stream(stream)
-        self.handle = ctypes.c_void_p(stream.cuda_stream)
 
     def __enter__(self):
         if self._ctx is not None:
@@ -629,25 +627,39 @@ class _On:
             self._ctx.__exit__(*exc)
 
 
-def _need_vec(t: torch.Tensor, name: str, n: Optional[int] = None) -> None:
-    _need(t, name, torch.int32)
-    if not t.is_contiguous() or (n is not None and t.numel() != n):
+def _at(t: torch.Tensor, name: str, dtype: torch.dtype, index: Optional[int] = None) -> int:
+    """The CUDA device index of t, a tensor of this type (on device `index` if given)."""
+    i = t.get_device()
+    if i < 0 or t.dtype is not dtype:
+        _need(t, name, dtype)
+    if index is not None and i != index:
+        raise MinisglError(f"tensors on different devices: {name} on cuda:{i}, others on cuda:{index}")
+    return i
+
+
+def _vec(t: torch.Tensor, name: str, n: Optional[int] = None, index: Optional[int] = None) -> int:
+    i = _at(t, name, torch.int32, index)
+    if (n is not None and t.numel() != n) or not t.is_contiguous():
         raise MinisglError(f"{name} must be a contiguous int32 tensor" + (f" of {n} elements" if n is not None else ""))
+    return i
 
 
-def _need_table(t: torch.Tensor, n: int) -> None:
-    _need(t, "page_table", torch.int32)
-    if t.dim() != 2 or t.shape[0] != n or (t.shape[1] > 1 and t.stride(1) != 1):
+def _table(t: torch.Tensor, n: int, index: Optional[int] = None) -> Tuple[int, int]:
+    """Row stride and width of a page table of n rows."""
+    _at(t, "page_table", torch.int32, index)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != n or (shape[1] > 1 and strides[1] != 1):
         raise MinisglError("page_table must be [B, W] with unit column stride")
+    # the stride of a table of one row means nothing and can be anything
+    return (strides[0] if n > 1 else max(strides[0], shape[1])), shape[1]
 
 
-def _pt_stride(t: torch.Tensor) -> int:
-    # the stride of a table of one row (or no column) means nothing and can be anything
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-
-
-def _tok_stride(t: torch.Tensor, row: int) -> int:
-    return t.stride(0) if t.shape[0] > 1 else row
+def _kv_rows(t: torch.Tensor, name: str, n: int, row: int, index: int, what: str = "n_tokens") -> int:
+    """Token stride of n contiguous rows of `row` bf16 elements."""
+    _at(t, name, torch.bfloat16, index)
+    if not _rows_ok(t, n, row):
+        raise MinisglError(f"{name} must be [{what}, H_kv, d] with contiguous rows")
+    return t.stride(0) if n > 1 else row
 
 
 class KVPoolFP4:
@@ -692,7 +704,8 @@ class KVPoolFP4:
             scale_layer_stride=scales.stride(1), scale_row_stride=scales.stride(2),
             num_layers=L, num_rows=R, num_kv_heads=H, head_dim=d, page_size=page_size,
             dtype=MINISGL_FP4, k_exp=p[0], v_exp=p[1]) for p in set(zip(*exps))}
-        self._by_layer = [at[p] for p in zip(*exps)]
+        self._by_layer = [ctypes.byref(at[p]) for p in zip(*exps)]
+        self._index = data.get_device()
 
     @classmethod
     def zeros(cls, num_layers: int, num_rows: int, num_kv_heads: int, head_dim: int, page_size: int = 1,
@@ -707,7 +720,7 @@ class KVPoolFP4:
     def _desc(self, layer: int):
         if not 0 <= layer < self.num_layers:
             raise MinisglError(f"layer {layer} outside [0, {self.num_layers})")
-        return ctypes.byref(self._by_layer[layer])
+        return self._by_layer[layer]
 
 
 def kv_pool_fp4_bytes(num_layers: int, num_kv_heads: int, head_dim: int, num_tokens: int) -> int:
@@ -739,26 +752,24 @@ def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, pa
     rows are dummy_row.  pages_used > len(free_pages) says that pages ran out
     (the tokens without one are on dummy_row)."""
     lib = load_library()
-    B = cached_lens.numel()
-    _need_vec(cached_lens, "cached_lens")
-    _need_vec(extend_lens, "extend_lens", B)
-    _need_vec(free_pages, "free_pages")
-    _need_table(page_table, B)
-    total = int(total_tokens)
+    B, total = cached_lens.numel(), int(total_tokens)
     if total < 0:
         raise MinisglError("total_tokens must not be negative")
-    given = () if out is None else tuple(out)
+    dev = _vec(cached_lens, "cached_lens")
+    _vec(extend_lens, "extend_lens", B, dev)
+    _vec(free_pages, "free_pages", None, dev)
+    stride, width = _table(page_table, B, dev)
     if out is not None:
         for t, nm, n in zip(out, Slots._fields, (total, total, B + 1, B, 1)):
-            _need_vec(t, nm, n)
-    with _On(stream, cached_lens, extend_lens, page_table, free_pages, *given) as st:
+            _vec(t, nm, n, dev)
+    with _On(stream, dev) as st:
         if out is None:
             out = Slots.empty(B, total, cached_lens.device)
-        _check(lib.minisgl_build_slots(_ptr(cached_lens), _ptr(extend_lens), B, _ptr(page_table),
-                                       _pt_stride(page_table), page_table.shape[1], _ptr(free_pages),
-                                       free_pages.numel(), int(page_size), int(dummy_row), _ptr(out.out_loc),
-                                       _ptr(out.positions), _ptr(out.q_offsets), _ptr(out.seq_lens),
-                                       _ptr(out.pages_used), total, st), "build_slots")
+        loc, pos, off, lens, used = out
+        _check(lib.minisgl_build_slots(cached_lens.data_ptr(), extend_lens.data_ptr(), B, page_table.data_ptr(),
+                                       stride, width, free_pages.data_ptr(), free_pages.numel(), page_size,
+                                       dummy_row, loc.data_ptr(), pos.data_ptr(), off.data_ptr(), lens.data_ptr(),
+                                       used.data_ptr(), total, st), "build_slots")
     return out
 
 
@@ -766,17 +777,13 @@ def minisgl_store_kv_fp4(pool: KVPoolFP4, layer: int, k: torch.Tensor, v: torch.
                          out_loc: torch.Tensor, stream=None) -> None:
     """Quantise k[i], v[i] ([n_tokens, H_kv, d] bf16) into row out_loc[i] of the 4-bit pool."""
     lib = load_library()
-    _need(k, "k", torch.bfloat16)
-    _need(v, "v", torch.bfloat16)
-    _need_vec(out_loc, "out_loc")
+    dev, row = pool._index, pool.num_kv_heads * pool.head_dim
     n = out_loc.numel()
-    row = pool.num_kv_heads * pool.head_dim
-    for t, nm in ((k, "k"), (v, "v")):
-        if not _rows_ok(t, n, row):
-            raise MinisglError(f"{nm} must be [n_tokens, H_kv, d] with contiguous rows")
-    with _On(stream, pool.data, k, v, out_loc) as st:
-        _check(lib.minisgl_store_kv_fp4(pool._desc(layer), layer, _ptr(k), _ptr(v), _tok_stride(k, row),
-                                        _tok_stride(v, row), _ptr(out_loc), n, st), "store_kv_fp4")
+    _vec(out_loc, "out_loc", None, dev)
+    ks, vs = _kv_rows(k, "k", n, row, dev), _kv_rows(v, "v", n, row, dev)
+    with _On(stream, dev) as st:
+        _check(lib.minisgl_store_kv_fp4(pool._desc(layer), layer, k.data_ptr(), v.data_ptr(), ks, vs,
+                                        out_loc.data_ptr(), n, st), "store_kv_fp4")
 
 
 def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, lens: torch.Tensor,
@@ -787,27 +794,26 @@ def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, l
     row offsets[r] of k_out and v_out ([total_tokens, H_kv, d], made here if
     not given; rows that no request fills are not written)."""
     lib = load_library()
-    B = lens.numel()
-    _need_table(page_table, B)
-    _need_vec(lens, "lens")
-    _need_vec(offsets, "offsets", B + 1)
-    total, H, d = int(total_tokens), pool.num_kv_heads, pool.head_dim
+    dev, H, d = pool._index, pool.num_kv_heads, pool.head_dim
+    B, total = lens.numel(), int(total_tokens)
     if total < 0:
         raise MinisglError("total_tokens must not be negative")
-    for t, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is not None:
-            _need(t, nm, torch.bfloat16)
-            if not _rows_ok(t, total, H * d):
-                raise MinisglError(f"{nm} must be [total_tokens, H_kv, d] with contiguous rows")
-    with _On(stream, pool.data, page_table, lens, offsets, k_out, v_out) as st:
+    stride, width = _table(page_table, B, dev)
+    _vec(lens, "lens", None, dev)
+    _vec(offsets, "offsets", B + 1, dev)
+    ks = vs = H * d
+    if k_out is not None:
+        ks = _kv_rows(k_out, "k_out", total, H * d, dev, "total_tokens")
+    if v_out is not None:
+        vs = _kv_rows(v_out, "v_out", total, H * d, dev, "total_tokens")
+    with _On(stream, dev) as st:
         if k_out is None:
             k_out = torch.empty((total, H, d), dtype=torch.bfloat16, device=lens.device)
         if v_out is None:
             v_out = torch.empty((total, H, d), dtype=torch.bfloat16, device=lens.device)
-        _check(lib.minisgl_load_kv_fp4(pool._desc(layer), layer, _ptr(page_table), B, _pt_stride(page_table),
-                                       page_table.shape[1], _ptr(lens), _ptr(offsets), total, _ptr(k_out),
-                                       _ptr(v_out), _tok_stride(k_out, H * d), _tok_stride(v_out, H * d), st),
-               "load_kv_fp4")
+        _check(lib.minisgl_load_kv_fp4(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
+                                       lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
+                                       v_out.data_ptr(), ks, vs, st), "load_kv_fp4")
     return k_out, v_out
 
 
@@ -825,26 +831,26 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
     """Decode attention of q [B, H_q, d] over each request's page_table row of
     the 4-bit pool.  Without a workspace the call allocates its own."""
     lib = load_library()
-    _need(q, "q", torch.bfloat16)
-    if q.dim() != 3 or not q.is_contiguous() or q.shape[2] != pool.head_dim:
+    dev = _at(q, "q", torch.bfloat16, pool._index)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pool.head_dim or not q.is_contiguous():
         raise MinisglError("q must be contiguous [B, H_q, head_dim]")
-    B, Hq, d = q.shape
-    _need_table(page_table, B)
-    _need_vec(seq_lens, "seq_lens", B)
+    B, Hq, _ = shape
+    stride, width = _table(page_table, B, dev)
+    _vec(seq_lens, "seq_lens", B, dev)
     if out is not None:
-        _need(out, "out", torch.bfloat16)
-        if out.shape != q.shape or not out.is_contiguous():
+        _at(out, "out", torch.bfloat16, dev)
+        if out.shape != shape or not out.is_contiguous():
             raise MinisglError("out must be contiguous with the shape of q")
-    if workspace is not None and (not workspace.is_cuda or not workspace.is_contiguous()):
-        raise MinisglError("workspace must be a contiguous CUDA tensor")
-    with _On(stream, pool.data, q, page_table, seq_lens, out, workspace) as st:
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise MinisglError("workspace must be a contiguous CUDA tensor on the pool's device")
+    with _On(stream, dev) as st:
         if out is None:
             out = torch.empty_like(q)
         if workspace is None:
             workspace = decode_workspace_fp4(B, Hq, pool, max_splits)
-        _check(lib.minisgl_decode_attn_fp4(pool._desc(layer), layer, _ptr(q), Hq, _ptr(page_table), B,
-                                           _pt_stride(page_table), page_table.shape[1], _ptr(seq_lens),
-                                           float(sm_scale), _ptr(out), _ptr(workspace),
-                                           workspace.numel() * workspace.element_size(), split_tokens, st),
+        _check(lib.minisgl_decode_attn_fp4(pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B,
+                                           stride, width, seq_lens.data_ptr(), sm_scale, out.data_ptr(),
+                                           workspace.data_ptr(), workspace.nbytes, split_tokens, st),
                "decode_attn_fp4")
     return out

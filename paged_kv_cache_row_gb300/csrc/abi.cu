@@ -214,11 +214,13 @@ int decode_args(minisgl::DecodeArgs &a, const char *who, int32_t num_kv_heads, i
     // the largest split count the workspace holds
     int splits = 0;
     if (workspace && ((reinterpret_cast<uintptr_t>(workspace) & 255u) == 0)) {
-        for (int s = 256; s >= 2; --s)
-            if (ws_bytes(batch, num_q_heads, num_kv_heads, head_dim, s) <= workspace_bytes) {
-                splits = s;
-                break;
-            }
+        int lo = 1, hi = 257;  // holds lo, does not hold hi
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (ws_bytes(batch, num_q_heads, num_kv_heads, head_dim, mid) <= workspace_bytes) lo = mid;
+            else hi = mid;
+        }
+        splits = lo;
     }
     if (splits < 2)
         return fail(MINISGL_ERR_WORKSPACE,
