@@ -657,9 +657,12 @@ def _table(t: torch.Tensor, n: int, index: Optional[int] = None) -> Tuple[int, i
 def _kv_rows(t: torch.Tensor, name: str, n: int, row: int, index: int, what: str = "n_tokens") -> int:
     """Token stride of n contiguous rows of `row` bf16 elements."""
     _at(t, name, torch.bfloat16, index)
-    if not _rows_ok(t, n, row):
+    shape, strides = t.shape, t.stride()
+    usual = (len(shape) == 3 and shape[0] == n and shape[1] * shape[2] == row and strides[2] == 1
+             and strides[1] == shape[2])
+    if not usual and not _rows_ok(t, n, row):
         raise MinisglError(f"{name} must be [{what}, H_kv, d] with contiguous rows")
-    return t.stride(0) if n > 1 else row
+    return strides[0] if n > 1 else row
 
 
 class KVPoolFP4:

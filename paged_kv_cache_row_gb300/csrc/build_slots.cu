@@ -20,6 +20,7 @@ namespace minisgl {
 namespace {
 
 constexpr int SLOT_THREADS = 256;
+constexpr int SLOT_U = 4;  // tokens per thread
 constexpr int SLOT_MAX_BATCH = 4096;
 constexpr int32_t SLOT_SAT = 1 << 30;
 
@@ -95,37 +96,65 @@ __global__ void __launch_bounds__(SLOT_THREADS) build_slots_kernel(SlotArgs a, i
     }
     __syncthreads();
 
+    // SLOT_U consecutive tokens per thread: the request of the first by search, of the next by walking on
     const int all = s_off[B];
-    const int64_t step = (int64_t)gridDim.x * SLOT_THREADS;
-    for (int64_t i64 = (int64_t)blockIdx.x * SLOT_THREADS + tid; i64 < a.total_tokens; i64 += step) {
-        const int i = (int)i64;
-        int row = a.dummy_row, p = 0;
-        if (i < all) {
-            int lo = 0, hi = B;  // the last request that starts at or before token i: s_off[lo] <= i < s_off[lo + 1]
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_off[mid] <= i) lo = mid; else hi = mid;
-            }
-            const int c = min(__ldg(a.cached_lens + lo), SLOT_SAT), start = max(c, 0);
-            p = sat_add(start, i - s_off[lo]);
-            int32_t *table = a.page_table + (int64_t)lo * a.pt_stride;
-            if (p < W) {
-                if (c >= 0) {
-                    const int pg = page_of(p);
-                    if (c > 0 && pg == page_of(c - 1)) {
-                        row = table[c - 1] + (p - (c - 1));
-                    } else {
-                        const int k = s_page[lo] + (pg - pages_for(c));
-                        if (k < a.num_free)
-                            row = (int)((uint32_t)__ldg(a.free_pages + k) * (uint32_t)a.page_size) +
-                                  (p - pg * a.page_size);
-                    }
-                }
-                table[p] = row;
+    const int64_t step = (int64_t)gridDim.x * SLOT_THREADS * SLOT_U;
+    for (int64_t base = ((int64_t)blockIdx.x * SLOT_THREADS + tid) * SLOT_U; base < a.total_tokens; base += step) {
+        int r = 0;
+        if (base < all) {
+            int hi = B;  // the last request that starts at or before the token: s_off[r] <= i < s_off[r + 1]
+            while (hi - r > 1) {
+                const int mid = (r + hi) >> 1;
+                if (s_off[mid] <= base) r = mid; else hi = mid;
             }
         }
-        a.out_loc[i] = row;
-        a.positions[i] = p;
+        int row[SLOT_U], pos[SLOT_U];  // row: what is known of it before the loads below
+        const int32_t *from[SLOT_U];   // where the rest of it comes from, or null
+        int32_t *to[SLOT_U];
+        bool fresh[SLOT_U];            // *from is a page number
+#pragma unroll
+        for (int u = 0; u < SLOT_U; ++u) {
+            row[u] = a.dummy_row;
+            pos[u] = 0;
+            from[u] = nullptr;
+            to[u] = nullptr;
+            fresh[u] = false;
+            const int64_t i64 = base + u;
+            if (i64 >= min(all, a.total_tokens)) continue;
+            const int i = (int)i64;
+            while (s_off[r + 1] <= i) ++r;
+            const int c = min(__ldg(a.cached_lens + r), SLOT_SAT), start = max(c, 0);
+            const int p = sat_add(start, i - s_off[r]);
+            pos[u] = p;
+            if (p >= W) continue;
+            int32_t *table = a.page_table + (int64_t)r * a.pt_stride;
+            to[u] = table + p;
+            if (c < 0) continue;
+            const int pg = page_of(p);
+            if (c > 0 && pg == page_of(c - 1)) {
+                row[u] = p - (c - 1);
+                from[u] = table + (c - 1);
+            } else {
+                const int k = s_page[r] + (pg - pages_for(c));
+                if (k < a.num_free) {
+                    row[u] = p - pg * a.page_size;
+                    from[u] = a.free_pages + k;
+                    fresh[u] = true;
+                }
+            }
+        }
+        int got[SLOT_U];
+#pragma unroll
+        for (int u = 0; u < SLOT_U; ++u) got[u] = from[u] ? *from[u] : 0;
+#pragma unroll
+        for (int u = 0; u < SLOT_U; ++u) {
+            row[u] += fresh[u] ? (int)((uint32_t)got[u] * (uint32_t)a.page_size) : got[u];
+            if (to[u]) *to[u] = row[u];
+            if (base + u < a.total_tokens) {
+                a.out_loc[base + u] = row[u];
+                a.positions[base + u] = pos[u];
+            }
+        }
     }
 }
 
@@ -134,7 +163,8 @@ cudaError_t launch_build_slots(const SlotArgs &a, cudaStream_t s) {
     if ((a.page_size & (a.page_size - 1)) == 0)
         for (shift = 0; (1 << shift) < a.page_size; ++shift) {
         }
-    int64_t blocks = ((int64_t)a.total_tokens + SLOT_THREADS - 1) / SLOT_THREADS;
+    constexpr int SPAN = SLOT_THREADS * SLOT_U;
+    int64_t blocks = ((int64_t)a.total_tokens + SPAN - 1) / SPAN;
     const int64_t cap = 4LL * max(device_sm_count(), 1);
     if (blocks > cap) blocks = cap;
     if (blocks < 1) blocks = 1;

@@ -30,6 +30,7 @@
 // 204 (174 then); one bulk copy (TMA) per row 396, about 41 cycles a copy and
 // SM, whatever its size; four producer warps, eight consumers and six stages
 // 164.
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -52,6 +53,10 @@ using fp4::TILE;
 template <int D, int NG>
 constexpr int MAX_WARPS = D == 128 && NG == 2 ? 8 : 16;
 constexpr int MAX_STAGES = 8;
+#ifndef WW
+#define WW 256
+#endif
+constexpr int WHOLE_WIDTH = WW;  // widest page table whose streams may be left whole
 constexpr long long WAIT_LIMIT = 1000000000LL;  // SM cycles (about 0.5 s)
 
 // How a CTA's warps and shared memory are laid out (set by the host).
@@ -59,6 +64,7 @@ struct Layout {
     int heads, subs, hblocks;   // KV heads at a time, groups of warps, head blocks
     int stages, stride;         // stages of a ring, bytes between token records
     int scale_bytes;            // piece of a scale row that one copy takes: 16, or d/16
+    int whole;                  // a group takes whole streams, at most one each: no schedule, no merge
     int off_bars, off_ring;
 };
 
@@ -120,7 +126,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     pdl_wait();
     pdl_launch_dependents();
     Schedule sch;
-    sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int64_t)gridDim.x * lay.subs);
+    sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int64_t)gridDim.x * lay.subs,
+             lay.whole);
     if (sch.total == 0) return;
 
     // warp (sub, head): the ring of its group
@@ -207,10 +214,29 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     uint32_t at = 0, parity = 0;  // stage to use
     const uint32_t my_k = ring + head_in * C::RB, my_s = ring + sk_off + head_in * C::SB;
     const int64_t seg_step = (int64_t)gridDim.x * lay.subs;
-    for (int64_t seg = (int64_t)blockIdx.x * lay.subs + sub; seg < sch.nseg; seg += seg_step) {
-        const int t0 = sch.begin(seg), t1 = sch.begin(seg + 1);
+    // neighbouring ranges on different SMs: few ranges spread over all of them
+    for (int64_t seg = blockIdx.x + (int64_t)sub * gridDim.x; seg < sch.nseg; seg += seg_step) {
+        int t0, t1;
         Cursor c, pc;  // the tile to use, the tile to fetch
-        sch.locate(c, t0);
+        if (lay.whole) {
+            c.r = (int)(seg / lay.hblocks);
+            c.hb = (int)(seg - (int64_t)c.r * lay.hblocks);
+            c.left = sch.len(c.r);
+            t0 = 0;
+            t1 = (c.left + TILE - 1) / TILE;
+            if (t1 == 0) {  // no context: zeros
+                const int head = c.hb * heads + head_in;
+                if (head < Hkv)
+                    for (int i = lane; i < G * D / 8; i += 32)
+                        st_v4(static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)c.r * Hq + head * G) * D + i * 8,
+                              make_uint4(0u, 0u, 0u, 0u));
+                continue;
+            }
+        } else {
+            t0 = sch.begin(seg);
+            t1 = sch.begin(seg + 1);
+            sch.locate(c, t0);
+        }
         pc = c;
         auto set_table = [&]() { table = a.page_table + (int64_t)pc.r * a.pt_stride + (sch.len(pc.r) - pc.left); };
         auto fetch_next = [&]() {  // only called when a next tile exists
@@ -223,12 +249,17 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
         };
         set_table();
         int todo = t1 - t0;  // tiles not asked for yet
+        // the first two tiles' page-table entries at once, then one tile ahead
+        int row = load_row(pc.left), hb = pc.hb;
         for (int i = 0; i < stages - 1 && todo > 0; ++i) {
-            issue(pc.hb, load_row(pc.left));
-            if (--todo > 0) fetch_next();
+            const int now = row, now_hb = hb;
+            if (--todo > 0) {
+                fetch_next();
+                row = load_row(pc.left);
+                hb = pc.hb;
+            }
+            issue(now_hb, now);
         }
-        int row = 0;
-        if (todo > 0) row = load_row(pc.left);
         bool open = true, from_start = c.left == sch.len(c.r);
         for (int t = t0; t < t1; ++t) {
             const int head = HEADS ? head_in : c.hb * heads + head_in;
@@ -246,10 +277,11 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
                 w.values(my_k + st + v_off, my_s + st + (sv_off - sk_off), stride, lane, pb);
             }
             if (todo > 0) {
-                issue(pc.hb, row);  // into the stage of the tile before this one
+                issue(hb, row);  // into the stage of the tile before this one
                 if (--todo > 0) {
                     fetch_next();
                     row = load_row(pc.left);  // for the next iteration
+                    hb = pc.hb;
                 }
             }
             __syncwarp();
@@ -265,7 +297,7 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
                     const bool whole = from_start && last;
                     const int split = whole ? 0 : (int)(seg - sch.range_of(sch.before(c.r, c.hb)));
                     w.close(a, (int64_t)c.r * Hq + head * G, G, whole, split, out_scale, lane);
-                    if (last && lane == 0) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
+                    if (last && lane == 0 && !lay.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
                 }
                 if (t + 1 < t1) sch.next_stream(c);
                 open = from_start = true;
@@ -331,15 +363,16 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, Layout lay, cudaStream_t s) {
     if (lay.stages > MAX_STAGES) lay.stages = MAX_STAGES;
     if (lay.stages < 2) return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)lay.off_ring + (size_t)lay.stages * lay.subs * TILE * lay.stride;
+    // Where every stream can have a group of its own and is short, it is left
+    // whole: no schedule to sum, no partials and no merge launch.
+    const int64_t sms = device_sm_count(), streams = (int64_t)a.batch * lay.hblocks;
+    lay.whole = a.pt_width <= WHOLE_WIDTH && streams <= sms * lay.subs && a.split_tokens == 0;
     // never more ranges than tiles could exist
-    const int64_t max_tiles = (int64_t)a.batch * lay.hblocks * ((a.pt_width + TILE - 1) / TILE);
-    int64_t grid = device_sm_count();
-    const int64_t need = (max_tiles + lay.subs - 1) / lay.subs;
-    if (grid > need) grid = need;
-    if (grid < 1) grid = 1;
+    const int64_t max_tiles = streams * ((a.pt_width + TILE - 1) / TILE);
+    const int64_t grid = std::max<int64_t>(1, std::min(sms, lay.whole ? streams : max_tiles));
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(lay.heads * lay.subs * 32), smem, s, args,
                    a.sm_scale * fp4::LOG2E * ldexpf(1.f, p.k_exp), ldexpf(1.f, p.v_exp), lay);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || lay.whole) return e;
     return launch_decode_merge(a, s);
 }
 

@@ -369,13 +369,21 @@ struct Schedule {
     int W, hblocks, chunks, total;
     int64_t nseg;
 
-    // Called by all threads of the CTA; s_prefix has room for schedule_ints(batch).
-    __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int64_t ranges) {
+    // Called by all threads of the CTA (it synchronises them); s_prefix has
+    // room for schedule_ints(batch).  whole: range i is stream i, nothing to sum.
+    __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int64_t ranges,
+                                         bool whole) {
         prefix = s_prefix;
         seq_lens = a.seq_lens;
         W = a.pt_width;
         hblocks = hblocks_;
         chunks = (a.batch + CHUNK - 1) / CHUNK;
+        if (whole) {
+            nseg = (int64_t)a.batch * hblocks;
+            total = 1;
+            __syncthreads();
+            return;
+        }
         // every thread sums the tiles of its chunks, then a scan over the CTA
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
         __shared__ int s_sum[32], s_max[32];

@@ -5,14 +5,23 @@
 //     a = max|x| * 2^-exp,  s = e4m3(a / 6),  c = e2m1(x * 2^-exp / s)
 // Every rounding is decided exactly.  x has 8 significant bits and 2^-exp
 // moves only its exponent.  A border between two e4m3 values has at most 5
-// bits, six times it 7, so a is either exactly on it or at least a relative
-// 2^-8 away: a / 6 rounded to fp32 falls on the same side.  A border between
-// two e2m1 values has at most 3 bits, times s 7, so x * 2^-exp / s too is
-// either exactly on a border or 2^-8 away from all of them.  x times the
-// rounded 1/s is within 2^-22 of the quotient; rounded once more, to 12
-// significant bits, it is exactly on the border in the first case and on the
-// right side of it in the second.
+// bits, six times it 7, so a / 6 is either exactly on it or at least a
+// relative 2^-8 away; a border between two e2m1 values has at most 3 bits,
+// times s 7, so the same holds for x * 2^-exp / s.  The quotient x / s is
+// formed from 1/s = r + t with r a little below 1/s and t = (1 - r s) r, the
+// first step of Newton's iteration: fma(x, r, x t) is within 2^-40 of it
+// before its one rounding, so a quotient that lies on a border comes out
+// exactly there, and every other on its own side.  r, t > 0 keep the sign of
+// a zero and let an infinity through (it saturates).
 // Load: the reverse, bf16(c * s * 2^exp), which is exact.
+//
+// Both are bound by HBM (2.56 bytes a channel) only if the arithmetic stays
+// near 8 instructions a channel.  So a thread keeps one column (K or V, and
+// the block) for all its tokens: the division of the index and the choice of
+// pointers happen once, not once per block, which took half of all issue
+// slots.
+#include <algorithm>
+
 #include "fp4.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -20,139 +29,226 @@
 namespace minisgl {
 
 namespace {
-constexpr int FP4_THREADS = 256;
+constexpr int MAX_THREADS = 512;
+constexpr int STORE_RESIDENT = 1536;  // threads per SM: 40 registers, one block of 16 per thread in
+                                      // flight (two took 64 registers and the same time)
+constexpr int LOAD_RESIDENT = 1024;   // threads per SM of the load kernel
+constexpr int LOAD_U = 4;             // blocks of 16 that a thread of it has in flight
+constexpr int LOAD_TOKENS = 128; // most tokens of a load tile
 
-// x to 12 significant bits, nearest; keeps signs and infinities
-__device__ __forceinline__ float round12(float x) {
-    return __uint_as_float((__float_as_uint(x) + 0x800u) & 0xfffff000u);
-}
 }  // namespace
 
-// blocks16: blocks of 16 per K (or V) row.  Item w: token, then K or V, then
-// the block, so neighbouring threads take neighbouring blocks of one row.
-__global__ void __launch_bounds__(FP4_THREADS) store_kv_fp4_kernel(StoreFp4Args a, uint32_t blocks16,
-                                                                   int log2_per_tok) {
-    pdl_wait();
-    pdl_launch_dependents();
-    const uint32_t per_tok = 2u * blocks16;
-    const uint32_t total = (uint32_t)a.n_tokens * per_tok;
-    for (uint32_t w = blockIdx.x * FP4_THREADS + threadIdx.x; w < total; w += gridDim.x * FP4_THREADS) {
-        const uint32_t i = log2_per_tok >= 0 ? w >> log2_per_tok : w / per_tok;
-        const uint32_t rem = w - i * per_tok;
-        const bool is_v = rem >= blocks16;
-        const uint32_t blk = is_v ? rem - blocks16 : rem;
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_v ? a.v : a.k) +
-                                   (int64_t)i * (is_v ? a.v_tok_stride : a.k_tok_stride) + blk * FP4_BLOCK;
-        const uint4 x0 = ld_nc_v4(src), x1 = ld_nc_v4(src + 8);
-        const uint32_t x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-        // max|x| on the bit patterns: infinity above every number, NaN above infinity
-        uint32_t m = 0;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) m = __vmaxu2(m, x[j] & 0x7fff7fffu);
-        m = max(m & 0xffffu, m >> 16);
-        const float unit = pow2i(-(is_v ? a.pool.v_exp : a.pool.k_exp));
-        const uint32_t sb = f32_to_e4m3(__fdiv_rn(__uint_as_float(m << 16) * unit, 6.f));
-        const float s = f16x2_to_f32(e4m3x2_to_f16x2(sb)).x;
-        const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-        float y[16];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            y[2 * j] = round12(__uint_as_float(x[j] << 16) * unit * inv);
-            y[2 * j + 1] = round12(__uint_as_float(x[j] & 0xffff0000u) * unit * inv);
-        }
-        int row = __ldg(a.out_loc + i);
-        // out-of-range rows are a caller error; clamp so the write stays in the pool
-        row = min(max(row, 0), a.pool.num_rows - 1);
-        *reinterpret_cast<uint2 *>((is_v ? a.pool.v_data : a.pool.k_data) + (int64_t)row * a.pool.data_stride +
-                                   blk * (FP4_BLOCK / 2)) = make_uint2(f32_to_e2m1x8(y), f32_to_e2m1x8(y + 8));
-        ((is_v ? a.pool.v_scale : a.pool.k_scale) + (int64_t)row * a.pool.scale_stride)[blk] = (uint8_t)sb;
+// 32 bytes from 32-byte (WIDE) or 16-byte aligned memory
+template <bool WIDE>
+__device__ __forceinline__ void ld_32(const void *p, uint32_t (&x)[8]) {
+    if constexpr (WIDE) {
+        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+                     : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
+                     : "l"(p));
+    } else {
+        const uint4 a = ld_nc_v4(p), b = ld_nc_v4(static_cast<const char *>(p) + 16);
+        x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void st_32(void *p, const uint32_t (&x)[8]) {
+    if constexpr (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                     "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+                     : "memory");
+    } else {
+        st_v4(p, make_uint4(x[0], x[1], x[2], x[3]));
+        st_v4(static_cast<char *>(p) + 16, make_uint4(x[4], x[5], x[6], x[7]));
     }
 }
 
-namespace {
+// 1/s = r + t to about 2^-40, for 2^-9 <= s <= 448
+__device__ __forceinline__ void split_reciprocal(float s, float &r, float &t) {
+    r = __fdividef(1.f, s) * (1.f - 0x1p-21f);  // below 1/s: the approximation is within 2 ulp
+    t = fmaf(-r, s, 1.f) * r;
+}
 
-// Tokens a block of the load kernel takes at a time.
-constexpr int LOAD_TOKENS = 32;
+// One block of 16: x (bf16) to e2m1 pairs c and the scale's byte.
+__device__ __forceinline__ void quantise16(const uint32_t (&x)[8], float unit, uint2 &c, uint32_t &sb) {
+    // max|x| (its sign comes out as the exclusive or); a NaN wins
+    uint32_t m = x[0];
+#pragma unroll
+    for (int j = 1; j < 8; ++j) asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;\n" : "+r"(m) : "r"(x[j]));
+    m &= 0x7fff7fffu;
+    m = max(m & 0xffffu, m >> 16);  // bit patterns order like the values, NaN above infinity
+    float r, t;
+    split_reciprocal(6.f, r, t);
+    const float a = __uint_as_float(m << 16) * unit;
+    sb = f32_to_e4m3(fmaf(a, r, a * t));
+    const float s = f16x2_to_f32(e4m3x2_to_f16x2(sb)).x;
+    split_reciprocal(s, r, t);
+    r = s > 0.f ? r * unit : 0.f;
+    t = s > 0.f ? t * unit : 0.f;
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float lo = __uint_as_float(x[j] << 16), hi = __uint_as_float(x[j] & 0xffff0000u);
+        y[2 * j] = fmaf(lo, r, lo * t);
+        y[2 * j + 1] = fmaf(hi, r, hi * t);
+    }
+    c = make_uint2(f32_to_e2m1x8(y), f32_to_e2m1x8(y + 8));
+}
 
-}  // namespace
-
-__global__ void __launch_bounds__(FP4_THREADS) load_kv_fp4_kernel(LoadFp4Args a, uint32_t blocks16) {
-    __shared__ int s_row[LOAD_TOKENS];  // pool row of each token, or -1
+// A block of threads has one thread per column (K blocks of 16, then V blocks)
+// of `toks` tokens; with more columns than threads (toks = 1) it goes over
+// them in steps.  A thread takes every (grid * toks)-th token.
+template <bool WIDE>
+__global__ void __launch_bounds__(MAX_THREADS, STORE_RESIDENT / MAX_THREADS) store_kv_fp4_kernel(StoreFp4Args a, int blocks16, int toks) {
     pdl_wait();
     pdl_launch_dependents();
-    const float k_unit = pow2i(a.pool.k_exp), v_unit = pow2i(a.pool.v_exp);
-    const uint32_t per_tok = 2u * blocks16;
-    const int64_t tiles = ((int64_t)a.total_tokens + LOAD_TOKENS - 1) / LOAD_TOKENS;
-    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const int64_t t0 = tile * LOAD_TOKENS;
-        if (threadIdx.x < LOAD_TOKENS) {
-            const int64_t t = t0 + threadIdx.x;
-            int row = -1;
-            if (t < a.total_tokens) {
+    const int sub = threadIdx.x / (2 * blocks16);
+    if (sub >= toks) return;
+    const int64_t step = (int64_t)gridDim.x * toks;
+    for (int col = threadIdx.x - sub * 2 * blocks16; col < 2 * blocks16; col += blockDim.x) {
+        const bool is_v = col >= blocks16;
+        const int blk = is_v ? col - blocks16 : col;
+        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_v ? a.v : a.k) + blk * FP4_BLOCK;
+        const int64_t tok_stride = is_v ? a.v_tok_stride : a.k_tok_stride;
+        uint8_t *data = (is_v ? a.pool.v_data : a.pool.k_data) + blk * (FP4_BLOCK / 2);
+        uint8_t *scale = (is_v ? a.pool.v_scale : a.pool.k_scale) + blk;
+        const float unit = pow2i(-(is_v ? a.pool.v_exp : a.pool.k_exp));
+        for (int64_t i = blockIdx.x * toks + sub; i < a.n_tokens; i += step) {
+            uint32_t x[8], sb;
+            uint2 c;
+            ld_32<WIDE>(src + i * tok_stride, x);
+            const int row = __ldg(a.out_loc + i);
+            quantise16(x, unit, c, sb);
+            // out-of-range rows are a caller error; clamp so the write stays in the pool
+            const uint32_t r = (uint32_t)min(max(row, 0), a.pool.num_rows - 1);
+            *reinterpret_cast<uint2 *>(data + (uint64_t)r * (uint32_t)a.pool.data_stride) = c;
+            scale[(uint64_t)r * (uint32_t)a.pool.scale_stride] = (uint8_t)sb;
+        }
+    }
+}
+
+// A block of the load kernel takes a run of tiles of tile_toks tokens, one
+// thread per column of `toks` tokens at a time.  Its first tile_toks threads
+// look up the pool rows of a tile before the block converts the one before
+// it: the request of a run's first tokens by binary search, the later ones by
+// walking on.
+template <bool WIDE>
+__global__ void __launch_bounds__(MAX_THREADS, LOAD_RESIDENT / MAX_THREADS)
+    load_kv_fp4_kernel(LoadFp4Args a, int blocks16, int toks, int tile_toks) {
+    __shared__ int s_row[2][LOAD_TOKENS];  // pool row of each token, or -1
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t tiles = ((int64_t)a.total_tokens + tile_toks - 1) / tile_toks;
+    const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
+    int req = -1;  // lane's request
+    auto look_up = [&](int64_t tile, int *rows) {
+        const int64_t t = tile * tile_toks + threadIdx.x;
+        int row = -1;
+        if (t < a.total_tokens) {
+            if (req < 0) {
                 int lo = 0, hi = a.batch;  // the last request with offsets[r] <= t
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
                     if (__ldg(a.offsets + mid) <= t) lo = mid; else hi = mid;
                 }
-                const int64_t j = t - __ldg(a.offsets + lo);
-                const int n = min(max(__ldg(a.lens + lo), 0), a.pt_width);
-                if (j >= 0 && j < n && t < __ldg(a.offsets + lo + 1))
-                    row = min(max(__ldg(a.page_table + lo * a.pt_stride + j), 0), a.pool.num_rows - 1);
+                req = lo;
             }
-            s_row[threadIdx.x] = row;
+            int end = __ldg(a.offsets + req + 1);
+            while (req + 1 < a.batch && end <= t) end = __ldg(a.offsets + ++req + 1);
+            const int64_t j = t - __ldg(a.offsets + req);
+            const int n = min(max(__ldg(a.lens + req), 0), a.pt_width);
+            if (j >= 0 && j < n && t < end)
+                row = min(max(__ldg(a.page_table + req * a.pt_stride + j), 0), a.pool.num_rows - 1);
         }
+        rows[threadIdx.x] = row;
+    };
+    const int sub = threadIdx.x / (2 * blocks16);
+    if ((int)threadIdx.x < tile_toks && first < last) look_up(first, s_row[0]);
+    for (int64_t tile = first; tile < last; ++tile) {
+        const int *rows = s_row[(tile - first) & 1];
         __syncthreads();
-        for (uint32_t w = threadIdx.x; w < LOAD_TOKENS * per_tok; w += FP4_THREADS) {
-            const uint32_t i = w / per_tok, rem = w - i * per_tok;
-            const int row = s_row[i];
-            if (row < 0) continue;
-            const bool is_v = rem >= blocks16;
-            const uint32_t blk = is_v ? rem - blocks16 : rem;
-            const uint2 c = *reinterpret_cast<const uint2 *>((is_v ? a.pool.v_data : a.pool.k_data) +
-                                                             (int64_t)row * a.pool.data_stride + blk * (FP4_BLOCK / 2));
-            const uint32_t sb = ((is_v ? a.pool.v_scale : a.pool.k_scale) + (int64_t)row * a.pool.scale_stride)[blk];
-            const uint32_t s = e4m3x2_to_f16x2(sb | (sb << 8));
-            const float unit = is_v ? v_unit : k_unit;
-            uint32_t h[2][4], o[8];
-            e2m1x8_to_f16x2(c.x, h[0]);
-            e2m1x8_to_f16x2(c.y, h[1]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = f16x2_to_f32(mul_f16x2(h[j >> 2][j & 3], s));
-                o[j] = pack_bf16x2(f.x * unit, f.y * unit);
-            }
+        if ((int)threadIdx.x < tile_toks && tile + 1 < last) look_up(tile + 1, s_row[(tile + 1 - first) & 1]);
+        if (sub >= toks) continue;
+        for (int col = threadIdx.x - sub * 2 * blocks16; col < 2 * blocks16; col += blockDim.x) {
+            const bool is_v = col >= blocks16;
+            const int blk = is_v ? col - blocks16 : col;
+            const uint8_t *data = (is_v ? a.pool.v_data : a.pool.k_data) + blk * (FP4_BLOCK / 2);
+            const uint8_t *scale = (is_v ? a.pool.v_scale : a.pool.k_scale) + blk;
+            const float unit = pow2i(is_v ? a.pool.v_exp : a.pool.k_exp);
+            const int64_t tok_stride = is_v ? a.v_tok_stride : a.k_tok_stride;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_v ? a.v_out : a.k_out) +
-                                 (t0 + i) * (is_v ? a.v_tok_stride : a.k_tok_stride) + blk * FP4_BLOCK;
-            st_v4(dst, make_uint4(o[0], o[1], o[2], o[3]));
-            st_v4(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
+                                 tile * tile_toks * tok_stride + blk * FP4_BLOCK;
+            for (int i0 = sub; i0 < tile_toks; i0 += LOAD_U * toks) {
+                uint2 c[LOAD_U];
+                uint32_t sb[LOAD_U];
+                int row[LOAD_U];
+#pragma unroll
+                for (int u = 0; u < LOAD_U; ++u) {
+                    const int i = i0 + u * toks;
+                    row[u] = i < tile_toks ? rows[i] : -1;
+                    if (row[u] >= 0) {
+                        const uint32_t r = (uint32_t)row[u];
+                        c[u] = __ldg(reinterpret_cast<const uint2 *>(data + (uint64_t)r * (uint32_t)a.pool.data_stride));
+                        sb[u] = __ldg(scale + (uint64_t)r * (uint32_t)a.pool.scale_stride);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < LOAD_U; ++u) {
+                    if (row[u] < 0) continue;
+                    const uint32_t s = e4m3x2_to_f16x2(sb[u] | (sb[u] << 8));
+                    uint32_t h[2][4], o[8];
+                    e2m1x8_to_f16x2(c[u].x, h[0]);
+                    e2m1x8_to_f16x2(c[u].y, h[1]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = f16x2_to_f32(mul_f16x2(h[j >> 2][j & 3], s));
+                        o[j] = pack_bf16x2(f.x * unit, f.y * unit);
+                    }
+                    st_32<WIDE>(dst + (i0 + u * toks) * tok_stride, o);
+                }
+            }
         }
-        __syncthreads();
     }
 }
 
+namespace {
+
+// Threads per block and tokens per block-wide step for this many columns.
+void block_shape(int columns, int &threads, int &toks) {
+    toks = columns < 256 ? 256 / columns : 1;
+    threads = (int)std::min<int64_t>(((int64_t)toks * columns + 31) / 32 * 32, MAX_THREADS);
+}
+
+bool aligned32(const void *p, int64_t tok_stride) {
+    return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && tok_stride % 16 == 0;
+}
+
+}  // namespace
+
 cudaError_t launch_store_kv_fp4(const StoreFp4Args &a, cudaStream_t s) {
     if (a.n_tokens == 0) return cudaSuccess;
-    const int64_t blocks16 = (int64_t)a.pool.num_kv_heads * a.pool.head_dim / FP4_BLOCK;
-    const int64_t per_tok = 2 * blocks16, total = a.n_tokens * per_tok;
-    if (total >= (int64_t(1) << 31)) return cudaErrorInvalidValue;  // the host refuses this first
-    int log2_per_tok = -1;
-    if ((per_tok & (per_tok - 1)) == 0)
-        for (log2_per_tok = 0; (int64_t(1) << log2_per_tok) < per_tok; ++log2_per_tok) {
-        }
-    int64_t blocks = (total + FP4_THREADS - 1) / FP4_THREADS;
-    const int64_t cap = (int64_t)device_sm_count() * 8;
+    const int blocks16 = a.pool.num_kv_heads * a.pool.head_dim / FP4_BLOCK;
+    int threads, toks;
+    block_shape(2 * blocks16, threads, toks);
+    int64_t blocks = ((int64_t)a.n_tokens + toks - 1) / toks;
+    const int64_t cap = (int64_t)device_sm_count() * (STORE_RESIDENT / threads);
     if (blocks > cap) blocks = cap;
-    return launch_pdl(store_kv_fp4_kernel, dim3((unsigned)blocks), dim3(FP4_THREADS), 0, s, a, (uint32_t)blocks16,
-                      log2_per_tok);
+    const bool wide = aligned32(a.k, a.k_tok_stride) && aligned32(a.v, a.v_tok_stride);
+    return launch_pdl(wide ? store_kv_fp4_kernel<true> : store_kv_fp4_kernel<false>, dim3((unsigned)blocks),
+                      dim3(threads), 0, s, a, blocks16, toks);
 }
 
 cudaError_t launch_load_kv_fp4(const LoadFp4Args &a, cudaStream_t s) {
     if (a.batch == 0 || a.total_tokens == 0) return cudaSuccess;
-    const int64_t blocks16 = (int64_t)a.pool.num_kv_heads * a.pool.head_dim / FP4_BLOCK;
-    int64_t blocks = ((int64_t)a.total_tokens + LOAD_TOKENS - 1) / LOAD_TOKENS;
-    const int64_t cap = (int64_t)device_sm_count() * 8;
-    if (blocks > cap) blocks = cap;
-    return launch_pdl(load_kv_fp4_kernel, dim3((unsigned)blocks), dim3(FP4_THREADS), 0, s, a, (uint32_t)blocks16);
+    const int blocks16 = a.pool.num_kv_heads * a.pool.head_dim / FP4_BLOCK;
+    int threads, toks;
+    block_shape(2 * blocks16, threads, toks);
+    // tiles as large as still give every resident block one; at least a step of the block
+    const int64_t cap = (int64_t)device_sm_count() * (LOAD_RESIDENT / threads);
+    const int tile = (int)std::min<int64_t>(LOAD_TOKENS, std::max<int64_t>(toks, (a.total_tokens + cap - 1) / cap));
+    const int64_t blocks = std::min(cap, ((int64_t)a.total_tokens + tile - 1) / tile);
+    const bool wide = aligned32(a.k_out, a.k_tok_stride) && aligned32(a.v_out, a.v_tok_stride);
+    return launch_pdl(wide ? load_kv_fp4_kernel<true> : load_kv_fp4_kernel<false>, dim3((unsigned)blocks),
+                      dim3(threads), 0, s, a, blocks16, toks, tile);
 }
 
 }  // namespace minisgl
