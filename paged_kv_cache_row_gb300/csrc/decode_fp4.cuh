@@ -367,12 +367,14 @@ struct Schedule {
     const int32_t *prefix;  // shared: tiles before request CHUNK * k, then all tiles
     const int32_t *seq_lens;
     int W, hblocks, chunks, total;
+    bool whole;             // range i is stream i
     int64_t nseg;
 
     // Called by all threads of the CTA (it synchronises them); s_prefix has
-    // room for schedule_ints(batch).  whole: range i is stream i, nothing to sum.
+    // room for schedule_ints(batch).  With whole there is nothing to sum.
     __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int64_t ranges,
-                                         bool whole) {
+                                         bool whole_) {
+        whole = whole_;
         prefix = s_prefix;
         seq_lens = a.seq_lens;
         W = a.pt_width;
@@ -461,6 +463,22 @@ struct Schedule {
         }
         c.hb = off / nt;
         c.left = len(c.r) - (off - c.hb * nt) * TILE;
+    }
+    // Tiles of range seg.
+    __device__ __forceinline__ int range_tiles(int64_t seg) const {
+        return whole ? tiles((int)(seg / hblocks)) : begin(seg + 1) - begin(seg);
+    }
+    // The same, and its first tile (with no tiles: the stream).
+    __device__ __forceinline__ int range(int64_t seg, Cursor &c) const {
+        if (whole) {
+            c.r = (int)(seg / hblocks);
+            c.hb = (int)(seg - (int64_t)c.r * hblocks);
+            c.left = len(c.r);
+            return (c.left + TILE - 1) / TILE;
+        }
+        const int t = begin(seg);
+        locate(c, t);
+        return begin(seg + 1) - t;
     }
     // To the first tile of the next stream (there is one).
     __device__ __forceinline__ void next_stream(Cursor &c) const {
