@@ -358,7 +358,7 @@ struct Cursor {
 
 // Every CTA derives the same schedule from seq_lens: the tiles of all streams
 // (request, head block) in a row, cut into nseg ranges whose lengths differ
-// by at most one tile.  The prefix sums are kept for every CHUNK-th request
+// by at most one tile (32-bit arithmetic: all tiles together are below 2^31).  The prefix sums are kept for every CHUNK-th request
 // only, so that they leave room for the rings at the largest batch.
 constexpr int CHUNK = 4;
 __host__ __device__ constexpr int schedule_ints(int batch) { return (batch + CHUNK - 1) / CHUNK + 2; }
@@ -366,22 +366,23 @@ __host__ __device__ constexpr int schedule_ints(int batch) { return (batch + CHU
 struct Schedule {
     const int32_t *prefix;  // shared: tiles before request CHUNK * k, then all tiles
     const int32_t *seq_lens;
-    int W, hblocks, chunks, total;
+    int batch, W, hblocks, chunks, total;
     bool whole;             // range i is stream i
-    int64_t nseg;
+    int nseg, each, more;   // ranges, tiles of each, how many have one more
 
     // Called by all threads of the CTA (it synchronises them); s_prefix has
     // room for schedule_ints(batch).  With whole there is nothing to sum.
-    __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int64_t ranges,
+    __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int ranges,
                                          bool whole_) {
         whole = whole_;
         prefix = s_prefix;
         seq_lens = a.seq_lens;
+        batch = a.batch;
         W = a.pt_width;
         hblocks = hblocks_;
         chunks = (a.batch + CHUNK - 1) / CHUNK;
         if (whole) {
-            nseg = (int64_t)a.batch * hblocks;
+            nseg = a.batch * hblocks;
             total = 1;
             __syncthreads();
             return;
@@ -389,13 +390,17 @@ struct Schedule {
         // every thread sums the tiles of its chunks, then a scan over the CTA
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
         __shared__ int s_sum[32], s_max[32];
-        const int each = (chunks + blockDim.x - 1) / blockDim.x;
-        const int k0 = min(tid * each, chunks), k1 = min(k0 + each, chunks);
+        const int share = (chunks + blockDim.x - 1) / blockDim.x;
+        const int k0 = min(tid * share, chunks), k1 = min(k0 + share, chunks);
         int mine = 0, mx = 0;
-        for (int r = k0 * CHUNK; r < min(k1 * CHUNK, a.batch); ++r) {
-            const int nt = tiles(r);
-            mine += nt;
-            mx = max(mx, nt);
+        for (int k = k0; k < k1; ++k) {
+            int nt[CHUNK];
+            chunk_tiles(k, nt);
+#pragma unroll
+            for (int q = 0; q < CHUNK; ++q) {
+                mine += nt[q];
+                mx = max(mx, nt[q]);
+            }
         }
         mine *= hblocks;
         int inc = mine;
@@ -415,7 +420,11 @@ struct Schedule {
         for (int w = 0; w < warp; ++w) at += s_sum[w];
         for (int k = k0; k < k1; ++k) {
             s_prefix[k] = at;
-            for (int r = k * CHUNK; each > 1 && r < min((k + 1) * CHUNK, a.batch); ++r) at += tiles(r) * hblocks;
+            if (share == 1) break;
+            int nt[CHUNK];
+            chunk_tiles(k, nt);
+#pragma unroll
+            for (int q = 0; q < CHUNK; ++q) at += nt[q] * hblocks;
         }
         if (tid == 0) {
             int all = 0, longest = 0;
@@ -428,24 +437,37 @@ struct Schedule {
         }
         __syncthreads();
         total = s_prefix[chunks];
-        // Ranges [seg * total / nseg, (seg + 1) * total / nseg), each at least
-        // L = total / nseg >= 1 tiles long.  A stream of nt tiles meets at most
-        // (nt - 2) / L + 2 of them, and L >= (nt - 1) / (max_splits - 1) keeps
-        // that within max_splits.
+        // nseg ranges of L = total / nseg >= 1 tiles, the first `more` with one
+        // more.  A stream of nt tiles meets at most (nt - 2) / L + 2 of them, and
+        // L >= (nt - 1) / (max_splits - 1) keeps that within max_splits.
         int want = a.split_tokens > 0 ? (int)(((int64_t)a.split_tokens + TILE - 1) / TILE) : 1;
         want = max(want, (s_prefix[chunks + 1] + a.max_splits - 2) / (a.max_splits - 1));
-        if (a.split_tokens > 0) ranges = total / want;
-        nseg = max((int64_t)1, min(ranges, (int64_t)(total / want)));
+        const int most = total / want;
+        nseg = max(1, a.split_tokens > 0 ? most : min(ranges, most));
+        each = total / nseg;
+        more = total - each * nseg;
     }
-    __device__ __forceinline__ int begin(int64_t seg) const { return (int)(seg * total / nseg); }
+    __device__ __forceinline__ int begin(int seg) const { return seg * each + min(seg, more); }
     // the range that holds tile t
-    __device__ __forceinline__ int64_t range_of(int t) const { return (((int64_t)t + 1) * nseg - 1) / total; }
+    __device__ __forceinline__ int range_of(int t) const {
+        const int longer = more * (each + 1);  // tiles of the longer ranges
+        return t < longer ? t / (each + 1) : more + (t - longer) / each;
+    }
     __device__ __forceinline__ int len(int r) const { return clamp_len(__ldg(seq_lens + r), W); }
     __device__ __forceinline__ int tiles(int r) const { return (len(r) + TILE - 1) / TILE; }
+    // the same of a chunk's requests, all loads at once
+    __device__ __forceinline__ void chunk_tiles(int k, int (&nt)[CHUNK]) const {
+#pragma unroll
+        for (int q = 0; q < CHUNK; ++q) nt[q] = k * CHUNK + q < batch ? __ldg(seq_lens + k * CHUNK + q) : 0;
+#pragma unroll
+        for (int q = 0; q < CHUNK; ++q) nt[q] = (clamp_len(nt[q], W) + TILE - 1) / TILE;
+    }
     // tiles before head block hb of request r
     __device__ __forceinline__ int before(int r, int hb) const {
-        int t = prefix[r / CHUNK] + hb * tiles(r);
-        for (int q = r - r % CHUNK; q < r; ++q) t += tiles(q) * hblocks;
+        int nt[CHUNK], t = prefix[r / CHUNK];
+        chunk_tiles(r / CHUNK, nt);
+#pragma unroll
+        for (int q = 0; q < CHUNK; ++q) t += nt[q] * (q < r % CHUNK ? hblocks : q == r % CHUNK ? hb : 0);
         return t;
     }
     __device__ __forceinline__ void locate(Cursor &c, int t) const {
@@ -454,25 +476,29 @@ struct Schedule {
             const int mid = (lo + hi) >> 1;
             if (prefix[mid] <= t) lo = mid; else hi = mid;
         }
-        int off = t - prefix[lo];
-        c.r = lo * CHUNK;
-        int nt = tiles(c.r);
-        while (off >= nt * hblocks) {
-            off -= nt * hblocks;
-            nt = tiles(++c.r);
-        }
-        c.hb = off / nt;
-        c.left = len(c.r) - (off - c.hb * nt) * TILE;
+        int off = t - prefix[lo], nt[CHUNK], q = 0;
+        chunk_tiles(lo, nt);
+        int n = nt[0];
+#pragma unroll
+        for (int i = 1; i < CHUNK; ++i)
+            if (q == i - 1 && off >= n * hblocks) {
+                off -= n * hblocks;
+                n = nt[i];
+                q = i;
+            }
+        c.r = lo * CHUNK + q;
+        c.hb = off / n;
+        c.left = len(c.r) - (off - c.hb * n) * TILE;
     }
     // Tiles of range seg.
-    __device__ __forceinline__ int range_tiles(int64_t seg) const {
-        return whole ? tiles((int)(seg / hblocks)) : begin(seg + 1) - begin(seg);
+    __device__ __forceinline__ int range_tiles(int seg) const {
+        return whole ? tiles(seg / hblocks) : begin(seg + 1) - begin(seg);
     }
     // The same, and its first tile (with no tiles: the stream).
-    __device__ __forceinline__ int range(int64_t seg, Cursor &c) const {
+    __device__ __forceinline__ int range(int seg, Cursor &c) const {
         if (whole) {
-            c.r = (int)(seg / hblocks);
-            c.hb = (int)(seg - (int64_t)c.r * hblocks);
+            c.r = seg / hblocks;
+            c.hb = seg - c.r * hblocks;
             c.left = len(c.r);
             return (c.left + TILE - 1) / TILE;
         }

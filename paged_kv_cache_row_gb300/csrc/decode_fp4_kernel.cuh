@@ -146,13 +146,12 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
     pdl_wait();
     pdl_launch_dependents();
     Schedule sch;
-    sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int64_t)gridDim.x * lay.subs,
-             lay.whole);
+    sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int)gridDim.x * lay.subs, lay.whole);
     if (sch.total == 0) return;
 
     const uint32_t all_bars = smem_u32(smem + lay.off_bars), all_rings = smem_u32(smem + lay.off_ring);
     constexpr int v_off = HEADS * C::RB, sk_off = 2 * v_off, sv_off = sk_off + HEADS * C::SB;
-    const int64_t seg_step = (int64_t)gridDim.x * lay.subs;
+    const int seg_step = (int)gridDim.x * lay.subs;
 
     if (warp >= CONSUMERS<D, NG>) {
         // ---- producers: step q = (round k, group s) fetches tile k of group s ----
@@ -181,7 +180,7 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
         bool have = off < HEADS * C::RB, shave = soff < HEADS * C::SB;  // the first block is full
 
         // lane s keeps group s's place: the next tile whose page-table entries are asked for
-        int64_t seg = blockIdx.x + (int64_t)lane * gridDim.x;
+        int seg = blockIdx.x + lane * (int)gridDim.x;
         int count = 0, in_range = 0;  // tiles in all, tiles left in the range
         Cursor c{0, 0, 0};
         const int32_t *table = a.page_table;  // entry of the tile's first token
@@ -193,7 +192,7 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
             if (in_range > 0) table = a.page_table + (int64_t)c.r * a.pt_stride + (sch.len(c.r) - c.left);
         };
         if (lane < lay.subs) {
-            for (int64_t g = seg; g < sch.nseg; g += seg_step) count += sch.range_tiles(g);
+            for (int g = seg; g < sch.nseg; g += seg_step) count += sch.range_tiles(g);
             enter();
         }
         int rounds = count;
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
     fp4::Stream<D, NG> w;
     uint32_t at = 0, parity = 0;  // stage to use
     // neighbouring ranges on different SMs: few ranges spread over all of them
-    for (int64_t seg = blockIdx.x + (int64_t)sub * gridDim.x; seg < sch.nseg; seg += seg_step) {
+    for (int seg = blockIdx.x + sub * (int)gridDim.x; seg < sch.nseg; seg += seg_step) {
         Cursor c;
         int todo = sch.range(seg, c);
         if (todo == 0) {  // a whole stream without context: zeros
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
                 const bool last = c.left <= 0;
                 if (!MULTI || live) {
                     const bool whole = from_start && last;
-                    const int split = whole ? 0 : (int)(seg - sch.range_of(sch.before(c.r, c.hb)));
+                    const int split = whole ? 0 : seg - sch.range_of(sch.before(c.r, c.hb));
                     w.close(a, (int64_t)c.r * Hq + head * G, G, whole, split, out_scale, lane);
                     if (last && lane == 0 && !sch.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
                 }
