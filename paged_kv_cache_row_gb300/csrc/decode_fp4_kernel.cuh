@@ -50,25 +50,10 @@ using fp4::Head;
 using fp4::Schedule;
 using fp4::TILE;
 
-// Warps of a CTA (one CTA per SM): 16 consumers, or 8 where two tiles of query
-// heads at d 128 need the registers, and 4 producers.  The registers that a
-// launch gives a thread are the same for all; the producers hand theirs over
-// (per warpgroup of 4 warps: 16 * 96 + 4 * 96 >= 16 * 104 + 4 * 40, and
-// 8 * 168 + 4 * 168 >= 8 * 224 + 4 * 40).
-constexpr int PRODUCERS = 4, PRODUCER_REGS = 40;
-constexpr int LOOKAHEAD = 4;  // steps whose page-table entries are in flight
+// Warps per CTA (one CTA per SM): 16 at up to 128 registers each; the 16-head
+// form at d 128 needs more.
 template <int D, int NG>
-constexpr int CONSUMERS = D == 128 && NG == 2 ? 8 : 16;
-template <int D, int NG>
-constexpr int CONSUMER_REGS = D == 128 && NG == 2 ? 224 : 104;
-template <int D, int NG>
-constexpr int THREADS = (CONSUMERS<D, NG> + PRODUCERS) * 32;
-
-template <int N>
-__device__ __forceinline__ void reg_alloc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_dealloc() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N)); }
-
+constexpr int MAX_WARPS = D == 128 && NG == 2 ? 8 : 16;
 constexpr int MAX_STAGES = 8;
 #ifndef WW
 #define WW 256
@@ -122,7 +107,7 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
 // us where 8 took 88 for the same bytes).  MULTI: there are several head
 // blocks (the sources move with them and the last may have fewer heads).
 template <int D, int NG, int HEADS, bool MULTI>
-__global__ void __launch_bounds__(THREADS<D, NG>, 1)
+__global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     decode_fp4_kernel(const DecodeFp4Args args, const float scale_log2, const float out_scale, const Layout lay) {
     using C = Head<D>;
     const DecodeArgs &a = args.d;
@@ -138,7 +123,7 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
 
     if ((int)threadIdx.x < lay.subs * stages) {  // full, empty of (ring, stage)
         const uint32_t b = smem_u32(smem + lay.off_bars) + threadIdx.x * 16u;
-        mbar_init(b, 32u * PRODUCERS);
+        mbar_init(b, 32u * HEADS);
         mbar_init(b + 8u, HEADS);
     }
     if (threadIdx.x == 0) s_abort = 0;
@@ -149,166 +134,103 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
     sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int)gridDim.x * lay.subs, lay.whole);
     if (sch.total == 0) return;
 
-    const uint32_t all_bars = smem_u32(smem + lay.off_bars), all_rings = smem_u32(smem + lay.off_ring);
-    constexpr int v_off = HEADS * C::RB, sk_off = 2 * v_off, sv_off = sk_off + HEADS * C::SB;
-    const int seg_step = (int)gridDim.x * lay.subs;
-
-    if (warp >= CONSUMERS<D, NG>) {
-        // ---- producers: step q = (round k, group s) fetches tile k of group s ----
-        reg_dealloc<PRODUCER_REGS>();
-        constexpr int SHARE = TILE / PRODUCERS;
-        const int tok0 = (warp - CONSUMERS<D, NG>) * SHARE;  // this warp's tokens of every tile
-        // The 16-byte pieces of a token's K and V rows are dealt to 2^LP lanes (K
-        // and V in one instruction, or one each), so a lane's piece is the same for
-        // every token; the same for the scales.
-        constexpr int HALF = HEADS * C::RB / 16, PIECES = 2 * HALF;
-        constexpr bool TWO = PIECES > 32;
-        constexpr int LP = TWO ? 5 : log2_up(PIECES), TOKS = 32 >> LP;
-        const int piece = lane & ((1 << LP) - 1), sub_tok = lane >> LP;
-        const bool is_v = !TWO && piece >= HALF;
-        const int off = !TWO && piece >= PIECES ? 1 << 30 : (is_v ? piece - HALF : piece) * 16;
-        const uint8_t *ksrc = (is_v ? pool.v_data : pool.k_data) + off, *vsrc = pool.v_data + off;
-        constexpr int WIDE = HEADS * C::SB % 16 == 0 ? 16 : C::SB;  // bytes of a scale piece
-        const bool narrow = WIDE == 16 && !lay.wide_scales;
-        constexpr int SHALF = HEADS * C::SB / WIDE, SPIECES = 2 * SHALF, SLP = log2_up(SPIECES), STOKS = 32 >> SLP;
-        const int sp = lane & ((1 << SLP) - 1), ssub_tok = lane >> SLP;
-        const bool s_is_v = sp >= SHALF;
-        const int soff = sp >= SPIECES ? 1 << 30 : (s_is_v ? sp - SHALF : sp) * WIDE;
-        const uint8_t *ssrc = (s_is_v ? pool.v_scale : pool.k_scale) + soff;
-        // the head block that the sources above belong to, and which of the lane's pieces it has
-        int in_hb = 0;
-        bool have = off < HEADS * C::RB, shave = soff < HEADS * C::SB;  // the first block is full
-
-        // lane s keeps group s's place: the next tile whose page-table entries are asked for
-        int seg = blockIdx.x + lane * (int)gridDim.x;
-        int count = 0, in_range = 0;  // tiles in all, tiles left in the range
-        Cursor c{0, 0, 0};
-        const int32_t *table = a.page_table;  // entry of the tile's first token
-        auto enter = [&]() {  // the next range with tiles in it
-            do {
-                in_range = seg < sch.nseg ? sch.range(seg, c) : -1;
-                seg += seg_step;
-            } while (in_range == 0);
-            if (in_range > 0) table = a.page_table + (int64_t)c.r * a.pt_stride + (sch.len(c.r) - c.left);
-        };
-        if (lane < lay.subs) {
-            for (int g = seg; g < sch.nseg; g += seg_step) count += sch.range_tiles(g);
-            enter();
-        }
-        int rounds = count;
-#pragma unroll
-        for (int o = 8; o; o >>= 1) rounds = max(rounds, __shfl_xor_sync(0xffffffffu, rounds, o));
-        rounds = __shfl_sync(0xffffffffu, rounds, 0);
-        const int steps = rounds * lay.subs;
-        int raw[LOOKAHEAD], hbs[LOOKAHEAD];  // of the next steps: lane i holds token tok0 + i's entry
-        int ask_k = 0, ask_s = 0;
-        auto ask = [&](int &entry, int &hb) {
-            if (ask_k < __shfl_sync(0xffffffffu, count, ask_s)) {
-                const int32_t *from = reinterpret_cast<const int32_t *>(
-                    __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(table), ask_s));
-                const int left = __shfl_sync(0xffffffffu, c.left, ask_s);
-                if constexpr (MULTI) hb = __shfl_sync(0xffffffffu, c.hb, ask_s);
-                entry = __ldg(from + min(tok0 + min(lane, SHARE - 1), left - 1));
-                if (lane == ask_s) {
-                    c.left -= TILE;
-                    table += TILE;
-                    if (--in_range == 0) {
-                        enter();
-                    } else if (c.left <= 0) {
-                        sch.next_stream(c);
-                        table = a.page_table + (int64_t)c.r * a.pt_stride;
-                    }
-                }
-            }
-            if (++ask_s == lay.subs) {
-                ask_s = 0;
-                ++ask_k;
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < LOOKAHEAD; ++i) {
-            raw[i] = hbs[i] = 0;
-            ask(raw[i], hbs[i]);
-        }
-        int k = 0, s = 0, stage = 0;
-        uint32_t parity = 1;  // of the empty barriers: the first round finds every stage free
-        for (int q0 = 0; q0 < steps; q0 += LOOKAHEAD) {
-#pragma unroll
-            for (int u = 0; u < LOOKAHEAD; ++u) {  // unrolled: an entry is not touched before its step
-                if (q0 + u >= steps) break;
-                const int row = min(max(raw[u], 0), a.num_rows - 1), hb = hbs[u];
-                ask(raw[u], hbs[u]);
-                if (k < __shfl_sync(0xffffffffu, count, s)) {
-                    if (MULTI && hb != in_hb) {
-                        const int d = (hb - in_hb) * HEADS, nh = min(HEADS, Hkv - hb * HEADS);
-                        ksrc += d * C::RB;
-                        vsrc += d * C::RB;
-                        ssrc += d * C::SB;
-                        have = off < nh * C::RB;
-                        shave = soff < nh * C::SB;
-                        in_hb = hb;
-                    }
-                    const uint32_t at = s * stages + stage, bar = all_bars + at * 16u;
-                    const uint32_t dst = all_rings + at * stage_bytes + tok0 * stride;
-                    guarded_wait(bar + 8u, parity, &s_abort);
-#pragma unroll
-                    for (int i0 = 0; i0 < SHARE; i0 += TOKS) {
-                        const int i = i0 + sub_tok;
-                        const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i & 31) * data_stride;
-                        const uint32_t to = dst + fp4::slot(i) * stride + piece * 16;
-                        if (i < SHARE && have) {
-                            cp_async_16(to, ksrc + e, 16);
-                            if constexpr (TWO) cp_async_16(to + HALF * 16, vsrc + e, 16);
-                        }
-                    }
-#pragma unroll
-                    for (int i0 = 0; i0 < SHARE; i0 += STOKS) {
-                        const int i = i0 + ssub_tok;
-                        const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i & 31) * scale_stride;
-                        const uint32_t to = dst + fp4::slot(i) * stride + sk_off + sp * WIDE;
-                        if (i < SHARE && shave) {
-                            if constexpr (WIDE == 16) {
-                                if (narrow) {  // rows that do not start on 16 bytes: d/16 bytes at a time
-                                    for (int b = 0; b < 16; b += C::SB) cp_async_small<C::SB>(to + b, ssrc + e + b);
-                                } else {
-                                    cp_async_16(to, ssrc + e, 16);
-                                }
-                            } else {
-                                cp_async_small<WIDE>(to, ssrc + e);
-                            }
-                        }
-                    }
-                    cp_async_arrive(bar);
-                }
-                if (++s == lay.subs) {
-                    s = 0;
-                    ++k;
-                    if (++stage == stages) {
-                        stage = 0;
-                        parity ^= 1;
-                    }
-                }
-            }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();  // nothing in flight when the CTA ends, even after a wait that ran out
-        return;
-    }
-
-    // ---- consumers: warp (group, head) ----
-    reg_alloc<CONSUMER_REGS<D, NG>>();
+    // warp (sub, head): the ring of its group
     const int head_in = warp % HEADS, sub = warp / HEADS;
-    if (sub >= lay.subs) return;
-    const uint32_t bars = all_bars + (uint32_t)(sub * stages) * 16u;
-    const uint32_t my_k = all_rings + (uint32_t)(sub * stages) * stage_bytes + head_in * C::RB;
-    const uint32_t my_s = all_rings + (uint32_t)(sub * stages) * stage_bytes + sk_off + head_in * C::SB;
+    const uint32_t bars = smem_u32(smem + lay.off_bars) + (uint32_t)(sub * stages) * 16u;
+    const uint32_t ring = smem_u32(smem + lay.off_ring) + (uint32_t)(sub * stages) * stage_bytes;
+    constexpr int v_off = HEADS * C::RB, sk_off = 2 * v_off, sv_off = sk_off + HEADS * C::SB;
+
+    // This warp fetches `mine` tokens of a tile: a run of them where that is a
+    // multiple of 8 tokens, else every HEADS-th.  Lane i holds the i-th one's
+    // page-table entry (past the end: the last token's).
+    constexpr bool RUN = HEADS <= 4 && TILE % HEADS == 0;
+    constexpr int MOST = (TILE + HEADS - 1) / HEADS;
+    const int mine = TILE % HEADS == 0 ? MOST : (TILE - head_in + HEADS - 1) / HEADS;
+    const int my_tok = min(RUN ? head_in * MOST + lane : head_in + HEADS * lane, TILE - 1);
+    auto slot_of = [&](int i) {  // of this warp's i-th token
+        return RUN ? head_in * MOST + fp4::slot(i)
+                   : HEADS == 8 ? fp4::slot(head_in) + 8 * i : fp4::slot(head_in + HEADS * i);
+    };
+    const int32_t *table = nullptr;  // entry of the first token of the tile to fetch
+    auto load_row = [&](int left) -> int { return __ldg(table + min(my_tok, left - 1)); };
+    // The 16-byte pieces of a token's K and V rows are dealt to 2^LP lanes (K
+    // and V in one instruction, or one each), so a lane's piece is the same for
+    // every token; the same for the scales.
+    constexpr int HALF = HEADS * C::RB / 16, PIECES = 2 * HALF;
+    constexpr bool TWO = PIECES > 32;
+    constexpr int LP = TWO ? 5 : log2_up(PIECES), TOKS = 32 >> LP;
+    const int piece = lane & ((1 << LP) - 1), sub_tok = lane >> LP;
+    const bool is_v = !TWO && piece >= HALF;
+    const int off = !TWO && piece >= PIECES ? 1 << 30 : (is_v ? piece - HALF : piece) * 16;
+    const uint8_t *ksrc = (is_v ? pool.v_data : pool.k_data) + off, *vsrc = pool.v_data + off;
+    constexpr int WIDE = HEADS * C::SB % 16 == 0 ? 16 : C::SB;  // bytes of a scale piece
+    const bool narrow = WIDE == 16 && !lay.wide_scales;
+    constexpr int SHALF = HEADS * C::SB / WIDE, SPIECES = 2 * SHALF, SLP = log2_up(SPIECES), STOKS = 32 >> SLP;
+    const int sp = lane & ((1 << SLP) - 1), ssub_tok = lane >> SLP;
+    const bool s_is_v = sp >= SHALF;
+    const int soff = sp >= SPIECES ? 1 << 30 : (s_is_v ? sp - SHALF : sp) * WIDE;
+    const uint8_t *ssrc = (s_is_v ? pool.v_scale : pool.k_scale) + soff;
+    // the head block that the sources above belong to, and which of the lane's pieces it has
+    int in_hb = 0;
+    bool have = off < HEADS * C::RB, shave = soff < HEADS * C::SB;  // the first block is full
+
+    uint32_t in_at = 0, in_parity = 1;  // stage to fill; the first round finds every stage empty
+    auto issue = [&](int hb, int raw) {
+        const int row = min(max(raw, 0), a.num_rows - 1);
+        const uint32_t bar = bars + in_at * 16u, dst = ring + in_at * stage_bytes;
+        if (MULTI && hb != in_hb) {
+            const int d = (hb - in_hb) * HEADS, nh = min(HEADS, Hkv - hb * HEADS);
+            ksrc += d * C::RB;
+            vsrc += d * C::RB;
+            ssrc += d * C::SB;
+            have = off < nh * C::RB;
+            shave = soff < nh * C::SB;
+            in_hb = hb;
+        }
+        guarded_wait(bar + 8u, in_parity, &s_abort);
+#pragma unroll
+        for (int i0 = 0; i0 < MOST; i0 += TOKS) {
+            const int i = i0 + sub_tok;
+            const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i & 31) * data_stride;
+            const uint32_t to = dst + slot_of(i) * stride + piece * 16;
+            if (i < mine && have) {
+                cp_async_16(to, ksrc + e, 16);
+                if constexpr (TWO) cp_async_16(to + HALF * 16, vsrc + e, 16);
+            }
+        }
+#pragma unroll
+        for (int i0 = 0; i0 < MOST; i0 += STOKS) {
+            const int i = i0 + ssub_tok;
+            const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i & 31) * scale_stride;
+            const uint32_t to = dst + slot_of(i) * stride + sk_off + sp * WIDE;
+            if (i < mine && shave) {
+                if constexpr (WIDE == 16) {
+                    if (narrow) {  // rows that do not start on 16 bytes: d/16 bytes at a time
+                        for (int k = 0; k < 16; k += C::SB) cp_async_small<C::SB>(to + k, ssrc + e + k);
+                    } else {
+                        cp_async_16(to, ssrc + e, 16);
+                    }
+                } else {
+                    cp_async_small<WIDE>(to, ssrc + e);
+                }
+            }
+        }
+        cp_async_arrive(bar);
+        if (++in_at == (uint32_t)stages) {
+            in_at = 0;
+            in_parity ^= 1;
+        }
+    };
+
     fp4::Stream<D, NG> w;
     uint32_t at = 0, parity = 0;  // stage to use
+    const uint32_t my_k = ring + head_in * C::RB, my_s = ring + sk_off + head_in * C::SB;
+    const int seg_step = (int)gridDim.x * lay.subs;
     // neighbouring ranges on different SMs: few ranges spread over all of them
     for (int seg = blockIdx.x + sub * (int)gridDim.x; seg < sch.nseg; seg += seg_step) {
-        Cursor c;
-        int todo = sch.range(seg, c);
-        if (todo == 0) {  // a whole stream without context: zeros
+        Cursor c, pc;  // the tile to use, the tile to fetch
+        int use = sch.range(seg, c);  // tiles not used yet
+        if (use == 0) {  // a whole stream without context: zeros
             const int head = c.hb * HEADS + head_in;
             if (head < Hkv)
                 for (int i = lane; i < G * D / 8; i += 32)
@@ -316,9 +238,32 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
                           make_uint4(0u, 0u, 0u, 0u));
             continue;
         }
+        pc = c;
+        auto set_table = [&]() { table = a.page_table + (int64_t)pc.r * a.pt_stride + (sch.len(pc.r) - pc.left); };
+        auto fetch_next = [&]() {  // only called when a next tile exists
+            pc.left -= TILE;
+            table += TILE;
+            if (pc.left <= 0) {
+                sch.next_stream(pc);
+                set_table();
+            }
+        };
+        set_table();
+        int todo = use;  // tiles not asked for yet
+        // the first two tiles' page-table entries at once, then one tile ahead
+        int row = load_row(pc.left), hb = pc.hb;
+        for (int i = 0; i < stages - 1 && todo > 0; ++i) {
+            const int now = row, now_hb = hb;
+            if (--todo > 0) {
+                fetch_next();
+                row = load_row(pc.left);
+                hb = pc.hb;
+            }
+            issue(now_hb, now);
+        }
         bool open = true, from_start = c.left == sch.len(c.r), live = false;
         int head = 0;
-        for (; todo > 0; --todo) {
+        for (; use > 0; --use) {
             if (open) {
                 open = false;
                 head = MULTI ? c.hb * HEADS + head_in : head_in;
@@ -333,6 +278,14 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
                 w.scores(my_k + st, my_s + st, stride, c.left, lane, pb);
                 w.values(my_k + st + v_off, my_s + st + (sv_off - sk_off), stride, lane, pb);
             }
+            if (todo > 0) {
+                issue(hb, row);  // into the stage of the tile before this one
+                if (--todo > 0) {
+                    fetch_next();
+                    row = load_row(pc.left);  // for the next iteration
+                    hb = pc.hb;
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(bars + at * 16u + 8u);
             if (++at == (uint32_t)stages) {
@@ -340,7 +293,7 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
                 parity ^= 1;
             }
             c.left -= TILE;
-            if (c.left <= 0 || todo == 1) {  // end of the stream or of the range
+            if (c.left <= 0 || use == 1) {  // end of the stream or of the range
                 const bool last = c.left <= 0;
                 if (!MULTI || live) {
                     const bool whole = from_start && last;
@@ -348,20 +301,19 @@ __global__ void __launch_bounds__(THREADS<D, NG>, 1)
                     w.close(a, (int64_t)c.r * Hq + head * G, G, whole, split, out_scale, lane);
                     if (last && lane == 0 && !sch.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
                 }
-                if (todo > 1) sch.next_stream(c);
+                if (use > 1) sch.next_stream(c);
                 open = from_start = true;
             }
         }
     }
+    cp_async_wait<0>();  // nothing in flight when the CTA ends, even after a wait that ran out
 }
 
 namespace {
 
-// The kernel's shared-memory limit raised to the device's, once per device;
-// refuses a kernel whose launch does not hold the registers that its warps
-// share out (setmaxnreg would wait for them for ever).
+// The kernel's shared-memory limit raised to the device's, once per device.
 template <typename K>
-cudaError_t prepare_kernel(K kernel, int threads, int shared_out, int &optin) {
+cudaError_t raise_limit(K kernel, int &optin) {
     struct Entry { const void *fn; int dev, optin; };
     static std::mutex mu;
     static Entry cache[64];
@@ -378,7 +330,6 @@ cudaError_t prepare_kernel(K kernel, int threads, int shared_out, int &optin) {
     cudaFuncAttributes fa;
     e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
-    if (e == cudaSuccess && fa.numRegs * threads < shared_out) return cudaErrorInvalidConfiguration;
     if (e == cudaSuccess) {
         optin -= (int)fa.sharedSizeBytes;
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
@@ -405,13 +356,11 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     auto kern = HEADS > 4 && lay.hblocks > 1 ? decode_fp4_kernel<D, NG, HEADS, (HEADS > 4)>
                                              : decode_fp4_kernel<D, NG, HEADS, false>;
     int optin = 0;
-    constexpr int consumers = CONSUMERS<D, NG> * 32;
-    cudaError_t e = prepare_kernel(kern, THREADS<D, NG>,
-                                   consumers * CONSUMER_REGS<D, NG> + PRODUCERS * 32 * PRODUCER_REGS, optin);
+    cudaError_t e = raise_limit(kern, optin);
     if (e != cudaSuccess) return e;
     // as many groups as leave three stages to each
     constexpr int stage = TILE * record_stride<D>(HEADS);
-    lay.subs = CONSUMERS<D, NG> / HEADS;
+    lay.subs = MAX_WARPS<D, NG> / HEADS;
     lay.off_bars = align_up(fp4::schedule_ints(a.batch) * 4, 16);
     lay.off_ring = align_up(lay.off_bars + MAX_STAGES * lay.subs * 16, 128);
     lay.subs = std::min(lay.subs, (optin - lay.off_ring) / (3 * stage));
@@ -425,7 +374,7 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     // never more ranges than tiles could exist
     const int64_t max_tiles = streams * ((a.pt_width + TILE - 1) / TILE);
     const int64_t grid = std::max<int64_t>(1, std::min(sms, lay.whole ? streams : max_tiles));
-    e = launch_pdl(kern, dim3((unsigned)grid), dim3(THREADS<D, NG>), smem, s, args,
+    e = launch_pdl(kern, dim3((unsigned)grid), dim3(HEADS * lay.subs * 32), smem, s, args,
                    a.sm_scale * fp4::LOG2E * ldexpf(1.f, p.k_exp), ldexpf(1.f, p.v_exp), lay);
     if (e != cudaSuccess || lay.whole) return e;
     return launch_decode_merge(a, s);
