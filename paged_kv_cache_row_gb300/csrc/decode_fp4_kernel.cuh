@@ -11,25 +11,34 @@
 // and the rows have to arrive without many requests: a head's row is only 64
 // + 8 bytes, in two places each for K and V.
 //
-// Work: tiles of 32 tokens of one request and up to 16 KV heads, one warp to
-// a head, so a token's row of all heads (contiguous) is fetched as one piece.
-// With fewer heads a CTA has several such groups of warps, each with a range
-// of tiles of its own.  The tiles of all requests are cut evenly over the
-// groups of all CTAs: contiguous ranges whose lengths differ by at most one.
+// Work: tiles of 32 tokens of one request and a block of up to 8 KV heads, one
+// warp to a head, so a token's row of these heads (contiguous) is fetched as
+// one piece.  A CTA (one per SM) has as many such groups of warps as fit 16
+// warps, each with a range of tiles of its own.  The tiles of all requests are
+// cut evenly over the groups of all CTAs: contiguous ranges whose lengths
+// differ by at most one.
 //
-// Loads: each group has a ring of stages with a full and an empty mbarrier
-// each.  The group's warps fetch a tile together, each its share of the
-// tokens, in 16-byte cp.async pieces: a warp instruction covers a token's K
-// row of eight heads (512 bytes at d 128), so few rows and lines are touched
-// at a time.  Page-table entries are read a tile before the rows they name.
+// Loads: each group has a ring of three or more stages with a full and an
+// empty mbarrier each.  The group's warps fetch a tile together, each its
+// share of the tokens, in 16-byte cp.async pieces: a warp instruction covers a
+// token's K row of eight heads (512 bytes at d 128), so few rows and lines are
+// touched at a time.  Page-table entries are read a tile before the rows they
+// name, and not looked at until then (a clamp right behind the load held its
+// warp for the load's latency once per tile: 174 us where 156 are taken now).
 // Rows past a request's end repeat its last row; their weights are zero.
 //
-// Arrangements timed and not kept, 256 requests of 1k to 8k tokens (8 KV
-// heads, d 128; this one takes 156 us): every warp fetching its own head's
-// 64- and 8-byte pieces 241; one barrier per tile instead of the mbarriers
-// 204 (174 then); one bulk copy (TMA) per row 396, about 41 cycles a copy and
-// SM, whatever its size; four producer warps, eight consumers and six stages
-// 164.
+// Measured (8 KV heads, d 128, warm): 256 requests of 1k to 8k tokens in
+// single-row pages 156 us, 5.2 TB/s of algorithmic bytes; 32 of 8k to 32k in
+// 64-row pages 149 us.  With the arithmetic left out 151 and 135, with the
+// loads left out 129 and 124: the two nearly balance, and about 10 us are the
+// start of the pipeline, the last ranges and the merge.
+//
+// Arrangements timed and not kept, on the first of these: every warp fetching
+// its own head's 64- and 8-byte pieces 241 us; one CTA barrier per tile for
+// the mbarriers 204 (174 then); one bulk copy (TMA) per row 396, about 41
+// cycles a copy and SM, whatever its size; four producer warps with eight
+// consumers and six stages 164, with sixteen consumers and registers shared
+// out 151, but 1.5 to 2.5 times slower at 1 and 2 heads.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -55,10 +64,6 @@ using fp4::TILE;
 template <int D, int NG>
 constexpr int MAX_WARPS = D == 128 && NG == 2 ? 8 : 16;
 constexpr int MAX_STAGES = 8;
-#ifndef WW
-#define WW 256
-#endif
-constexpr int WHOLE_WIDTH = WW;  // widest page table whose streams may be left whole
 constexpr long long WAIT_LIMIT = 1000000000LL;  // SM cycles (about 0.5 s)
 
 // How a CTA's warps and shared memory are laid out (set by the host).
@@ -367,12 +372,17 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     if (lay.subs < 1) return cudaErrorInvalidConfiguration;
     lay.stages = std::min((optin - lay.off_ring) / (lay.subs * stage), MAX_STAGES);
     const size_t smem = (size_t)lay.off_ring + (size_t)lay.stages * lay.subs * stage;
-    // Where every stream can have a group of its own and is short, it is left
-    // whole: no schedule to sum, no partials and no merge launch.
+    // Where every stream can have a group of its own it may be left whole: no
+    // schedule to sum, no partials, no merge launch, which saves about the time
+    // of 5 tiles.  A group then has up to `wide` tiles one after the other
+    // instead of its share of all tiles.  8 heads, d 128, whole against split:
+    // 16 requests 8.5 / 8.7 us at 128 tokens, 13.5 / 9.6 at 256; 256 requests
+    // 37 / 43 at 512, 67.5 / 68.6 at 1024.
     const int64_t sms = device_sm_count(), streams = (int64_t)a.batch * lay.hblocks;
-    lay.whole = a.pt_width <= WHOLE_WIDTH && streams <= sms * lay.subs && a.split_tokens == 0;
+    const int64_t groups = sms * lay.subs, wide = (a.pt_width + TILE - 1) / TILE;
+    lay.whole = streams <= groups && (wide - 5) * groups <= wide * streams && a.split_tokens == 0;
     // never more ranges than tiles could exist
-    const int64_t max_tiles = streams * ((a.pt_width + TILE - 1) / TILE);
+    const int64_t max_tiles = streams * wide;
     const int64_t grid = std::max<int64_t>(1, std::min(sms, lay.whole ? streams : max_tiles));
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(HEADS * lay.subs * 32), smem, s, args,
                    a.sm_scale * fp4::LOG2E * ldexpf(1.f, p.k_exp), ldexpf(1.f, p.v_exp), lay);

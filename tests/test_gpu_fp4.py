@@ -332,6 +332,39 @@ def test_decode_head_layouts(Hq, Hkv, d):
     check_decode(pool, q, pt, lens)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 2, 64), (16, 8, 128), (32, 2, 128), (11, 11, 128), (7, 7, 64), (20, 10, 64)])
+def test_decode_short_tables(Hq, Hkv, d):
+    """Tables narrow enough for every request to be left whole."""
+    for lens in ([0, 1, 31, 32, 33, 100, 128, 0], [5], [0], [1] * 40 + [32] * 3):
+        pool, q, pt = make_decode(Hq, Hkv, d, lens, 200, Hq + Hkv + d)
+        check_decode(pool, q, pt, lens)
+
+
+@pytest.mark.parametrize("H,d", [(8, 128), (2, 128), (4, 64), (16, 128), (3, 64)])
+def test_scale_rows_that_start_anywhere(H, d):
+    """Scale rows only d/16-byte aligned (a slice of wider rows), elements in
+    rows of all layers (pages outermost): store, load and decode."""
+    L, R, SB = 2, 150, d // 16
+    data = torch.zeros((2, R, L, H, d // 2), dtype=torch.uint8, device=DEV).transpose(1, 2)
+    scales = torch.zeros((2, L, R, H + 1, SB), dtype=torch.uint8, device=DEV)[:, :, :, 1:]
+    pool = mk.KVPoolFP4(data, scales, k_exp=[0, -2], v_exp=[0, -1])
+    n, lens = 130, [50, 80]
+    rows = np.random.default_rng(1).permutation(R)[:n]
+    check_store(pool, 1, kv_like((n, H, d), 1).to(DEV), kv_like((n, H, d), 2).to(DEV), rows)
+    pt = np.zeros((2, 96), dtype=int)
+    pt[0, :50], pt[1, :80] = rows[:50], rows[50:]
+    kv = pool_values(pool, 1)
+    k, v = mk.minisgl_load_kv_fp4(pool, 1, i32(pt), i32(lens), i32([0, 50, 130]), n)
+    assert np.array_equal(k.double().cpu().numpy(), kv[0][rows])
+    assert np.array_equal(v.double().cpu().numpy(), kv[1][rows])
+    q = kv_like((2, 2 * H, d), 3).to(DEV)
+    for split in (0, 32):
+        o = mk.minisgl_decode_attn_fp4(pool, 1, q, i32(pt), i32(lens), d ** -0.5, split_tokens=split)
+        want, mag, top = ref.decode(ref.bf16_to_f64(q), kv[0], kv[1], pt, lens, d ** -0.5)
+        bound = ref.decode_bound(want, mag, top, np.abs(kv[1]).max(), 80)
+        assert (np.abs(o.double().cpu().numpy() - want) <= bound).all()
+
+
 @pytest.mark.parametrize("split", [1, 32, 48, 100, 10 ** 6])
 @pytest.mark.parametrize("max_splits", [2, 5, 64, 256])
 def test_decode_split_counts(split, max_splits):
