@@ -115,6 +115,17 @@ struct Stream {
     float o[C::MT][NG][4];
     uint32_t qb[NG][C::KS][2];
 
+    // Asks L1 for the queries that open() will load: G rows from row0.
+    __device__ __forceinline__ void prefetch(const DecodeArgs &a, int64_t row0, int G, bool live, int lane) const {
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+            const int h = n * 8 + (lane >> 2);
+            if (h < G && live)
+                asm volatile("prefetch.global.L1 [%0];\n" ::"l"(static_cast<const __nv_bfloat16 *>(a.q) + (row0 + h) * D +
+                                                                (lane & 3) * C::QPT));
+        }
+    }
+
     // Loads the group's queries (q: G rows of D; null leaves zeros) and clears the sums.
     __device__ __forceinline__ void open(const __nv_bfloat16 *q, int G, float scale_log2, int lane) {
         const int lg = lane >> 2, lt = lane & 3;
@@ -128,7 +139,7 @@ struct Stream {
                 const __nv_bfloat16 *src = q + h * D + lt * C::QPT;
 #pragma unroll
                 for (int i = 0; i < C::QPT / 8; ++i) {
-                    const uint4 v = ld_nc_v4(src + 8 * i);
+                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
                     w[4 * i] = v.x;
                     w[4 * i + 1] = v.y;
                     w[4 * i + 2] = v.z;

@@ -251,6 +251,9 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
             if (pc.left <= 0) {
                 sch.next_stream(pc);
                 set_table();
+                // its queries, wanted when this tile is used (67 -> 64 us at 1000 requests of 17 to 300 tokens)
+                w.prefetch(a, (int64_t)pc.r * Hq + (MULTI ? pc.hb * HEADS + head_in : head_in) * G, G,
+                           !MULTI || pc.hb * HEADS + head_in < Hkv, lane);
             }
         };
         set_table();
