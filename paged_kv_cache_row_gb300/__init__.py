@@ -599,6 +599,22 @@ FP4_BLOCK = 16  # channels that share a scale
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
+# torch.empty_strided on the current CUDA device without its argument parser:
+# a call of 5 outputs takes 16 us instead of 21.
+_empty_cuda = getattr(getattr(torch._C, "_dynamo", None) and getattr(torch._C._dynamo, "guards", None),
+                      "_empty_strided_cuda", None)
+
+
+def _new(shape: Tuple[int, ...], dtype: torch.dtype, index: int) -> torch.Tensor:
+    """An uninitialised contiguous tensor on the current device, cuda:index."""
+    if _empty_cuda is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
+    strides, step = [], 1
+    for n in reversed(shape):
+        strides.append(step)
+        step *= n
+    return _empty_cuda(shape, tuple(reversed(strides)), dtype)
+
 
 class _On:
     """The stream a call runs on, with its device (and a stream that the caller
@@ -767,7 +783,9 @@ def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, pa
             _vec(t, nm, n, dev)
     with _On(stream, dev) as st:
         if out is None:
-            out = Slots.empty(B, total, cached_lens.device)
+            i32 = torch.int32
+            out = Slots(_new((total,), i32, dev), _new((total,), i32, dev), _new((B + 1,), i32, dev),
+                        _new((B,), i32, dev), _new((1,), i32, dev))
         loc, pos, off, lens, used = out
         _check(lib.minisgl_build_slots(cached_lens.data_ptr(), extend_lens.data_ptr(), B, page_table.data_ptr(),
                                        stride, width, free_pages.data_ptr(), free_pages.numel(), page_size,
@@ -811,9 +829,9 @@ def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, l
         vs = _kv_rows(v_out, "v_out", total, H * d, dev, "total_tokens")
     with _On(stream, dev) as st:
         if k_out is None:
-            k_out = torch.empty((total, H, d), dtype=torch.bfloat16, device=lens.device)
+            k_out = _new((total, H, d), torch.bfloat16, dev)
         if v_out is None:
-            v_out = torch.empty((total, H, d), dtype=torch.bfloat16, device=lens.device)
+            v_out = _new((total, H, d), torch.bfloat16, dev)
         _check(lib.minisgl_load_kv_fp4(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
                                        lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
                                        v_out.data_ptr(), ks, vs, st), "load_kv_fp4")
@@ -849,7 +867,7 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
         raise MinisglError("workspace must be a contiguous CUDA tensor on the pool's device")
     with _On(stream, dev) as st:
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(tuple(shape), torch.bfloat16, dev)
         if workspace is None:
             workspace = decode_workspace_fp4(B, Hq, pool, max_splits)
         _check(lib.minisgl_decode_attn_fp4(pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B,
