@@ -871,7 +871,7 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
         if workspace is None:
             workspace = decode_workspace_fp4(B, Hq, pool, max_splits)
         _check(lib.minisgl_decode_attn_fp4(pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B,
-                                           stride, width, seq_lens.data_ptr(), sm_scale, out.data_ptr(),
+                                           stride, width, seq_lens.data_ptr(), float(sm_scale), out.data_ptr(),
                                            workspace.data_ptr(), workspace.nbytes, split_tokens, st),
                "decode_attn_fp4")
     return out

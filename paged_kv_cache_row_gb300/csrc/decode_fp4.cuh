@@ -34,7 +34,7 @@ namespace fp4 {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
-constexpr float REF_START = -1e30f;  // below every finite score: the first tile sets the reference
+constexpr float REF_START = -3.402823466e38f;  // no finite score is below: the first tile sets the reference
 constexpr float REF_BELOW = 8.f;     // the reference starts this far below the maximum (base 2)
 constexpr float REF_ROOM = 15.f;     // and moves when a score passes it by more: 2^15 fits fp16
 
@@ -228,13 +228,17 @@ struct Stream {
         // ---- softmax weights; this lane holds tokens lg + 8*i (i < 4) ----
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
-            float x[2][4];  // [e][token]: scores less the reference, then weights
+            // [e][token]: scores less the reference, then weights.  The scores are
+            // rounded before the subtraction: in one fma the largest could come
+            // out half a unit of its last place (8 and more from 2^27 on) off
+            // the reference that is made of it.
+            float x[2][4];
             auto relative = [&]() {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        x[e][i] = fmaf(sa[i >> 1][n][2 * (i & 1) + e], sc[n][e], -ref[n][e]);
+                        x[e][i] = __fsub_rn(__fmul_rn(sa[i >> 1][n][2 * (i & 1) + e], sc[n][e]), ref[n][e]);
                 if (left < 32) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
@@ -265,6 +269,11 @@ struct Stream {
                     }
                 }
                 relative();
+                // from 2^27 on the reference itself may be rounded to 16 below; a NaN stays
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[e][i] = x[e][i] > REF_ROOM ? REF_ROOM : x[e][i];
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e)

@@ -404,6 +404,32 @@ def test_decode_sharp_scores():
     check_decode(pool, q, pt, lens, sm_scale=0.0)
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [16, 23, 27, 31, 60, 112])
+def test_decode_scores_of_any_size(power, sign):
+    """Equal keys with scores from 2^20 to near fp32's largest: equal weights,
+    so the mean of V, however coarse the scores' last place is."""
+    lens = [1, 5, 33, 120]
+    pool, q, pt = make_decode(8, 2, 64, lens, 200, 47)
+    pool.data[0] = pool.data[0, :, :1] & 0x77  # one row of positive elements
+    pool.scales[0] = pool.scales[0, :, :1]
+    q = (q.abs() * sign * 2.0 ** power).contiguous()
+    k, v = pool_values(pool)
+    o = mk.minisgl_decode_attn_fp4(pool, 0, q, i32(pt), i32(lens), 0.125).double().cpu().numpy()
+    for r, n in enumerate(lens):
+        rows = v[pt[r, :n]].repeat(4, axis=1)
+        want, mag = rows.mean(0), np.abs(rows).mean(0)
+        bound = ref.decode_bound(want, mag, np.zeros(8), np.nanmax(np.abs(v)), n)
+        assert (np.abs(o[r] - want) <= bound).all(), r
+    # split: V is one row too
+    pool.data[1] = pool.data[1, :, :1]
+    pool.scales[1] = pool.scales[1, :, :1]
+    pt = np.zeros((1, 2016))
+    want = pool_values(pool)[1][0].repeat(4, axis=0)
+    o = mk.minisgl_decode_attn_fp4(pool, 0, q[:1], i32(pt), i32([2000]), np.float32(0.125)).double().cpu().numpy()[0]
+    assert (np.abs(o - want) <= ref.decode_bound(want, np.abs(want), np.zeros(8), np.abs(want).max(), 2000)).all()
+
+
 @pytest.mark.parametrize("power", [-120, -40, 40, 100])
 def test_decode_query_and_pool_ranges(power):
     """q from far below to far above fp16's range against the opposite scale
