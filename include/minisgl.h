@@ -536,8 +536,8 @@ int minisgl_load_kv_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const in
 /*
  * Decode attention over the 4-bit pool: the definition, arguments and limits
  * of minisgl_decode_attn (q and out bf16, n == 0 gives out = 0) with K and V
- * the values of the pool's rows.  Products accumulate in fp32; softmax
- * weights are rounded to fp16 (11 bits) for the product with V.
+ * the values of the pool's rows, and pt_width <= 2^30.  Products accumulate
+ * in fp32; softmax weights are rounded to fp16 (11 bits) for the product with V.
  * workspace: as for minisgl_decode_attn (minisgl_decode_workspace_bytes);
  * nothing in it needs to start at zero, and calls that may run at the same
  * time need different workspaces.

@@ -757,7 +757,7 @@ bool overlap32(const int32_t *a, int64_t na, const int32_t *b, int64_t nb) {
     return x < y + (uintptr_t)nb * 4 && y < x + (uintptr_t)na * 4;
 }
 
-constexpr int64_t SLOT_MAX = int64_t(1) << 30;
+constexpr int64_t SLOT_MAX = int64_t(1) << 30;  // most tokens of a step, widest page table
 
 }  // namespace
 
@@ -889,6 +889,7 @@ int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, cons
     g_err.clear();
     NvtxRange nvtx_range("minisgl_decode_attn_fp4");
     if (int rc = check_pool_fp4(pool, layer, "decode_attn_fp4")) return rc;
+    if (pt_width > SLOT_MAX) return fail(MINISGL_ERR_UNSUPPORTED, "decode_attn_fp4: pt_width above 2^30");
     minisgl::DecodeFp4Args a;
     if (int rc = decode_args(a.d, "decode_attn_fp4", pool->num_kv_heads, pool->head_dim, pool->num_rows, q,
                              num_q_heads, page_table, batch, pt_row_stride, pt_width, seq_lens, sm_scale, out,

@@ -144,6 +144,10 @@ def test_decode_refusals(lib):
     assert call(11, None) == -6 and call(11, FAKE + 128) == -6 and call(12, need - 1) == -6
     assert b"decode_attn_fp4" in lib.minisgl_last_error()
     assert call(13, -1) == -1
+    wide = list(good)
+    for width in ((1 << 30) + 1, (1 << 31) - 1):
+        wide[6], wide[7] = 1 << 31, width
+        assert f(*wide) == -4
     assert call(5, 0) == 0
 
 
