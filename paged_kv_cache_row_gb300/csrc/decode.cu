@@ -607,15 +607,11 @@ cudaError_t launch_cfg(const DecodeArgs &a, cudaStream_t s) {
     cudaError_t e = launch_pdl(kern, dim3((unsigned)grid), dim3(warps * 32), smem, s, a,
                                a.sm_scale * LOG2E, prefix_bytes, stage_bytes);
     if (e != cudaSuccess || a.partials_only) return e;
-    return launch_decode_merge(a, s);
+    return launch_pdl(decode_merge_kernel<D>, dim3((a.batch * a.num_q_heads + 3) / 4), dim3(128), 0,
+                      s, a);
 }
 
 }  // namespace
-
-cudaError_t launch_decode_merge(const DecodeArgs &a, cudaStream_t s) {
-    return launch_pdl(a.head_dim == 128 ? decode_merge_kernel<128> : decode_merge_kernel<64>,
-                      dim3((a.batch * a.num_q_heads + 3) / 4), dim3(128), 0, s, a);
-}
 
 cudaError_t launch_decode(const DecodeArgs &a, cudaStream_t s) {
     if (a.batch == 0) return cudaSuccess;

@@ -3,7 +3,7 @@
 //     out[r,h] = sum_j softmax_j(sm_scale <q[r,h], K_j>) V_j,   j < seq_len[r],
 // K_j and V_j the values c * s * 2^exp of row page_table[r, j] (the pool's
 // format is in the public header).  Split partials are merged by
-// decode_merge_kernel, as for the bf16 pool.
+// decode_fp4_merge_kernel.
 //
 // What bounds it: the K/V bytes, 2 * (d/2 + d/16) a token and KV head, 144 at
 // d 128.  At the card's copy rate that is 43 elements a cycle and SM, so the
@@ -28,8 +28,8 @@
 // Rows past a request's end repeat its last row; their weights are zero.
 //
 // Measured (8 KV heads, d 128, warm): 256 requests of 1k to 8k tokens in
-// single-row pages 156 us, 5.2 TB/s of algorithmic bytes; 32 of 8k to 32k in
-// 64-row pages 149 us.  With the arithmetic left out 151 and 135, with the
+// single-row pages 154 us, 5.2 TB/s of algorithmic bytes; 32 of 8k to 32k in
+// 64-row pages 145 us.  With the arithmetic left out 151 and 135, with the
 // loads left out 129 and 124: the two nearly balance, and about 10 us are the
 // start of the pipeline, the last ranges and the merge.
 //
@@ -319,6 +319,71 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
 
 namespace {
 
+// Joins the partials of the streams that were cut, one warp per (request, query
+// head) row: out = sum_k w_k O_k / sum_k w_k, w_k = e^(LSE_k - max LSE).  Rows
+// that are whole hold their output already; empty requests get zeros.
+//
+// What bounds it are rounds of dependent loads, about 1 us each behind the
+// launch, and how many rows are under way.  There are two rounds: the length
+// and the count, then the LSEs and MOST partials.  MOST 16 takes 96 registers
+// and so 2432 rows at once, MOST 4 takes 40 and three times as many: the decode
+// of 1024 rows in 2-3 partials takes 44.6 / 45.5 us, of 2048 rows in about 10
+// 145.4 / 146.9, of 8192 rows in 2-3 156.6 / 153.9.
+template <int D, int MOST>
+__global__ void __launch_bounds__(128, MOST > 8 ? 4 : 12) decode_fp4_merge_kernel(const DecodeArgs a) {
+    constexpr int CPL = D / 32;  // channels per lane
+    const int Hkv = a.num_kv_heads, Hq = a.num_q_heads;
+    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (row >= a.batch * Hq) return;
+    const int r = row / Hq, g = (row - r * Hq) / (Hq / Hkv);
+    const int len = a.seq_lens[r], cnt = a.split_count[(int64_t)r * Hkv + g];
+    const int n = fp4::clamp_len(len, a.pt_width) == 0 ? 0 : min(cnt, a.max_splits);  // no count without context
+    if (n == 1) return;
+    const int64_t base = (int64_t)row * a.max_splits;
+    const float l0 = lane < n ? a.ws_lse[base + lane] : -INFINITY;
+    float M = l0;
+    for (int s = 32 + lane; s < n; s += 32) M = fmaxf(M, a.ws_lse[base + s]);
+    const float *src = a.ws_o + base * D + lane * CPL;  // of partial k at src + k * D
+    float acc[CPL], tot = n == 0 ? 1.f : 0.f;
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
+    for (int k0 = 0; k0 < n; k0 += MOST) {
+        float x[MOST][CPL];
+#pragma unroll
+        for (int k = 0; k < MOST; ++k)
+            if (k0 + k < n) {
+                if constexpr (CPL == 4) {
+                    const float4 v = *reinterpret_cast<const float4 *>(src + (k0 + k) * D);
+                    x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+                } else {
+                    const float2 v = *reinterpret_cast<const float2 *>(src + (k0 + k) * D);
+                    x[k][0] = v.x, x[k][1] = v.y;
+                }
+            }
+        if (k0 == 0) {  // while the first rows come
+#pragma unroll
+            for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        }
+        // the weights, in the first MOST lanes
+        const float w = lane < MOST && k0 + lane < n ? __expf((k0 ? a.ws_lse[base + k0 + lane] : l0) - M) : 0.f;
+#pragma unroll
+        for (int k = 0; k < MOST; ++k)
+            if (k0 + k < n) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                tot += wk;
+#pragma unroll
+                for (int c = 0; c < CPL; ++c) acc[c] += wk * x[k][c];
+            }
+    }
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)row * D + lane * CPL;
+    const float inv = 1.f / tot;
+#pragma unroll
+    for (int c = 0; c < CPL; c += 2)
+        *reinterpret_cast<uint32_t *>(out + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
+}
+
 // The kernel's shared-memory limit raised to the device's, once per device.
 template <typename K>
 cudaError_t raise_limit(K kernel, int &optin) {
@@ -390,7 +455,9 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(HEADS * lay.subs * 32), smem, s, args,
                    a.sm_scale * fp4::LOG2E * ldexpf(1.f, p.k_exp), ldexpf(1.f, p.v_exp), lay);
     if (e != cudaSuccess || lay.whole) return e;
-    return launch_decode_merge(a, s);
+    const int64_t rows = (int64_t)a.batch * a.num_q_heads;  // up to 4 CTAs of 4 an SM: the wide form
+    return launch_pdl(rows <= 16 * sms ? decode_fp4_merge_kernel<D, 16> : decode_fp4_merge_kernel<D, 4>,
+                      dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a);
 }
 
 }  // namespace

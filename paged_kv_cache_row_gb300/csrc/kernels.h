@@ -214,8 +214,6 @@ struct DecodeFp4Args {
     Fp4Layer pool;
 };
 cudaError_t launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t s);
-// The log-sum-exp merge of split partials (reads a's workspace parts).
-cudaError_t launch_decode_merge(const DecodeArgs &a, cudaStream_t s);
 
 int device_sm_count();
 

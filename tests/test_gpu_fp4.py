@@ -390,6 +390,15 @@ def test_decode_many_requests():
     check_decode(pool, q, pt, lens)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 2, 64), (16, 8, 128)])
+def test_decode_split_into_many_rows(Hq, Hkv, d):
+    """More query rows than one wave of the merge's wide form."""
+    lens = [(r * 37) % 190 for r in range(200)]
+    pool, q, pt = make_decode(Hq, Hkv, d, lens, 300, 29)
+    check_decode(pool, q, pt, lens, split_tokens=32)
+    check_decode(pool, q, pt, lens, split_tokens=32, max_splits=3)
+
+
 def test_decode_sharp_scores():
     """Scores spread over hundreds, rising and falling along the context, so
     that the running reference moves many times, and a negative scale."""
