@@ -594,53 +594,25 @@ def minisgl_check_shared_prefix(page_table: torch.Tensor, lens: torch.Tensor, sh
 FP4_BLOCK = 16  # channels that share a scale
 
 
-# The current stream's handle for a device index (torch.cuda.current_stream
-# builds a Stream object first, which takes longer than a kernel launch).
+# The quick forms of torch.cuda.current_stream(i).cuda_stream (which builds a
+# Stream object first and takes longer than a kernel launch), current_device()
+# and empty_strided(device="cuda"), where torch has them: a call that allocates
+# 5 outputs takes 15 us instead of 22.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-# torch.empty_strided on the current CUDA device without its argument parser:
-# a call of 5 outputs takes 16 us instead of 21.
-_empty_cuda = getattr(getattr(torch._C, "_dynamo", None) and getattr(torch._C._dynamo, "guards", None),
-                      "_empty_strided_cuda", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or \
+    (lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda"))
 
 
-def _new(shape: Tuple[int, ...], dtype: torch.dtype, index: int) -> torch.Tensor:
-    """An uninitialised contiguous tensor on the current device, cuda:index."""
-    if _empty_cuda is None:
-        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", index))
-    strides, step = [], 1
-    for n in reversed(shape):
-        strides.append(step)
-        step *= n
-    return _empty_cuda(shape, tuple(reversed(strides)), dtype)
-
-
-class _On:
-    """The stream a call runs on, with its device (and a stream that the caller
-    named) current for the call's own allocations and launches."""
-    __slots__ = ("handle", "_ctx")
-
-    def __init__(self, stream, index: int):
-        self._ctx = None
-        if stream is None:
-            self.handle = _raw_stream(index)
-            if torch.cuda.current_device() != index:
-                self._ctx = torch.cuda.device(index)
-        else:
-            if stream.device.index != index:
-                raise MinisglError(f"stream on {stream.device}, tensors on cuda:{index}")
-            self.handle = stream.cuda_stream
-            self._ctx = torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _on(stream, index: int):
+    """The context in which tensors on cuda:index are current: their device,
+    and the stream if the caller named one."""
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise MinisglError(f"stream on {stream.device}, tensors on cuda:{index}")
+    return torch.cuda.stream(stream)
 
 
 def _at(t: torch.Tensor, name: str, dtype: torch.dtype, index: Optional[int] = None) -> int:
@@ -770,41 +742,44 @@ def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, pa
     (into `out` if given).  cached_lens[r] < 0 marks a padding request, whose
     rows are dummy_row.  pages_used > len(free_pages) says that pages ran out
     (the tokens without one are on dummy_row)."""
-    lib = load_library()
     B, total = cached_lens.numel(), int(total_tokens)
     if total < 0:
         raise MinisglError("total_tokens must not be negative")
     dev = _vec(cached_lens, "cached_lens")
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_build_slots(cached_lens, extend_lens, page_table, free_pages, page_size, dummy_row,
+                                       total, out)
     _vec(extend_lens, "extend_lens", B, dev)
     _vec(free_pages, "free_pages", None, dev)
     stride, width = _table(page_table, B, dev)
     if out is not None:
         for t, nm, n in zip(out, Slots._fields, (total, total, B + 1, B, 1)):
             _vec(t, nm, n, dev)
-    with _On(stream, dev) as st:
-        if out is None:
-            i32 = torch.int32
-            out = Slots(_new((total,), i32, dev), _new((total,), i32, dev), _new((B + 1,), i32, dev),
-                        _new((B,), i32, dev), _new((1,), i32, dev))
-        loc, pos, off, lens, used = out
-        _check(lib.minisgl_build_slots(cached_lens.data_ptr(), extend_lens.data_ptr(), B, page_table.data_ptr(),
-                                       stride, width, free_pages.data_ptr(), free_pages.numel(), page_size,
-                                       dummy_row, loc.data_ptr(), pos.data_ptr(), off.data_ptr(), lens.data_ptr(),
-                                       used.data_ptr(), total, st), "build_slots")
+    else:
+        i32, one = torch.int32, (1,)
+        out = Slots(_new((total,), one, i32), _new((total,), one, i32), _new((B + 1,), one, i32),
+                    _new((B,), one, i32), _new(one, one, i32))
+    loc, pos, off, lens, used = out
+    _check(load_library().minisgl_build_slots(
+        cached_lens.data_ptr(), extend_lens.data_ptr(), B, page_table.data_ptr(), stride, width,
+        free_pages.data_ptr(), free_pages.numel(), page_size, dummy_row, loc.data_ptr(), pos.data_ptr(),
+        off.data_ptr(), lens.data_ptr(), used.data_ptr(), total, _raw_stream(dev)), "build_slots")
     return out
 
 
 def minisgl_store_kv_fp4(pool: KVPoolFP4, layer: int, k: torch.Tensor, v: torch.Tensor,
                          out_loc: torch.Tensor, stream=None) -> None:
     """Quantise k[i], v[i] ([n_tokens, H_kv, d] bf16) into row out_loc[i] of the 4-bit pool."""
-    lib = load_library()
     dev, row = pool._index, pool.num_kv_heads * pool.head_dim
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_store_kv_fp4(pool, layer, k, v, out_loc)
     n = out_loc.numel()
     _vec(out_loc, "out_loc", None, dev)
     ks, vs = _kv_rows(k, "k", n, row, dev), _kv_rows(v, "v", n, row, dev)
-    with _On(stream, dev) as st:
-        _check(lib.minisgl_store_kv_fp4(pool._desc(layer), layer, k.data_ptr(), v.data_ptr(), ks, vs,
-                                        out_loc.data_ptr(), n, st), "store_kv_fp4")
+    _check(load_library().minisgl_store_kv_fp4(pool._desc(layer), layer, k.data_ptr(), v.data_ptr(), ks, vs,
+                                               out_loc.data_ptr(), n, _raw_stream(dev)), "store_kv_fp4")
 
 
 def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, lens: torch.Tensor,
@@ -814,27 +789,26 @@ def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, l
     """Rows page_table[r, :lens[r]] of the 4-bit pool as bf16, request r's from
     row offsets[r] of k_out and v_out ([total_tokens, H_kv, d], made here if
     not given; rows that no request fills are not written)."""
-    lib = load_library()
     dev, H, d = pool._index, pool.num_kv_heads, pool.head_dim
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_load_kv_fp4(pool, layer, page_table, lens, offsets, total_tokens, k_out, v_out)
     B, total = lens.numel(), int(total_tokens)
     if total < 0:
         raise MinisglError("total_tokens must not be negative")
     stride, width = _table(page_table, B, dev)
     _vec(lens, "lens", None, dev)
     _vec(offsets, "offsets", B + 1, dev)
-    ks = vs = H * d
-    if k_out is not None:
-        ks = _kv_rows(k_out, "k_out", total, H * d, dev, "total_tokens")
-    if v_out is not None:
-        vs = _kv_rows(v_out, "v_out", total, H * d, dev, "total_tokens")
-    with _On(stream, dev) as st:
-        if k_out is None:
-            k_out = _new((total, H, d), torch.bfloat16, dev)
-        if v_out is None:
-            v_out = _new((total, H, d), torch.bfloat16, dev)
-        _check(lib.minisgl_load_kv_fp4(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
-                                       lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
-                                       v_out.data_ptr(), ks, vs, st), "load_kv_fp4")
+    row = H * d
+    ks = row if k_out is None else _kv_rows(k_out, "k_out", total, row, dev, "total_tokens")
+    vs = row if v_out is None else _kv_rows(v_out, "v_out", total, row, dev, "total_tokens")
+    if k_out is None:
+        k_out = _new((total, H, d), (row, d, 1), torch.bfloat16)
+    if v_out is None:
+        v_out = _new((total, H, d), (row, d, 1), torch.bfloat16)
+    _check(load_library().minisgl_load_kv_fp4(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
+                                              lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
+                                              v_out.data_ptr(), ks, vs, _raw_stream(dev)), "load_kv_fp4")
     return k_out, v_out
 
 
@@ -851,27 +825,29 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
                             max_splits: int = 32, stream=None) -> torch.Tensor:
     """Decode attention of q [B, H_q, d] over each request's page_table row of
     the 4-bit pool.  Without a workspace the call allocates its own."""
-    lib = load_library()
     dev = _at(q, "q", torch.bfloat16, pool._index)
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_decode_attn_fp4(pool, layer, q, page_table, seq_lens, sm_scale, out, workspace,
+                                           split_tokens, max_splits)
     shape = q.shape
     if len(shape) != 3 or shape[2] != pool.head_dim or not q.is_contiguous():
         raise MinisglError("q must be contiguous [B, H_q, head_dim]")
-    B, Hq, _ = shape
+    B, Hq, d = shape
     stride, width = _table(page_table, B, dev)
     _vec(seq_lens, "seq_lens", B, dev)
-    if out is not None:
+    if out is None:
+        out = _new((B, Hq, d), (Hq * d, d, 1), torch.bfloat16)
+    else:
         _at(out, "out", torch.bfloat16, dev)
         if out.shape != shape or not out.is_contiguous():
             raise MinisglError("out must be contiguous with the shape of q")
-    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+    if workspace is None:
+        workspace = decode_workspace_fp4(B, Hq, pool, max_splits)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise MinisglError("workspace must be a contiguous CUDA tensor on the pool's device")
-    with _On(stream, dev) as st:
-        if out is None:
-            out = _new(tuple(shape), torch.bfloat16, dev)
-        if workspace is None:
-            workspace = decode_workspace_fp4(B, Hq, pool, max_splits)
-        _check(lib.minisgl_decode_attn_fp4(pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B,
-                                           stride, width, seq_lens.data_ptr(), float(sm_scale), out.data_ptr(),
-                                           workspace.data_ptr(), workspace.nbytes, split_tokens, st),
-               "decode_attn_fp4")
+    _check(load_library().minisgl_decode_attn_fp4(
+        pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B, stride, width, seq_lens.data_ptr(),
+        float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, split_tokens,
+        _raw_stream(dev)), "decode_attn_fp4")
     return out
