@@ -24,7 +24,7 @@
 // token's K row of eight heads (512 bytes at d 128), so few rows and lines are
 // touched at a time.  Page-table entries are read a tile before the rows they
 // name, and not looked at until then (a clamp right behind the load held its
-// warp for the load's latency once per tile: 174 us where 156 are taken now).
+// warp for the load's latency once per tile: 174 us where 154 are taken now).
 // Rows past a request's end repeat its last row; their weights are zero.
 //
 // Measured (8 KV heads, d 128, warm): 256 requests of 1k to 8k tokens in
