@@ -2,6 +2,8 @@
 tests/fp4_ref.py.  Slots, stored bytes and loaded values must be equal; decode
 attention stays within bounds counted from its roundings (fp4_ref.decode_bound)."""
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -274,6 +276,20 @@ def test_load_many_short_requests():
     assert np.array_equal(v.double().cpu().numpy(), kv[1][rows])
 
 
+@pytest.mark.parametrize("H,d", [(33, 128), (40, 128), (130, 64)])
+def test_rows_wider_than_a_block_of_threads(H, d):
+    """Store, load and decode with more than 512 blocks of 16 in a token's row."""
+    n = 40
+    pool = mk.KVPoolFP4.zeros(1, 64, H, d, k_exp=-2, v_exp=-2)
+    at = np.random.default_rng(H).permutation(64)[:n]
+    k, v = kv_like((n, H, d), H).to(DEV), kv_like((n, H, d), H + 1).to(DEV)
+    check_store(pool, 0, k, v, at)
+    kv = pool_values(pool)
+    for got, want in zip(mk.minisgl_load_kv_fp4(pool, 0, i32(at[None]), i32([n]), i32([0, n]), n), kv):
+        assert np.array_equal(got.double().cpu().numpy(), want[at])
+    check_decode(pool, kv_like((1, H, d), 5).to(DEV), at[None], [n])
+
+
 def test_load_every_value():
     """Every element under every scale, at exponents whose values bf16 holds."""
     R = 256
@@ -544,6 +560,36 @@ def test_calls_on_a_named_stream():
         torch.full((1 << 22,), 255, dtype=torch.uint8, device=DEV)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+FIRST_USE = """
+import torch, paged_kv_cache_row_gb300 as mk
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+H, d, n = 2, 64, 70
+pool = mk.KVPoolFP4.zeros(1, 81, H, d, 4, k_exp=-2, v_exp=-2)
+kv = [torch.randn(n, H, d, device="cuda").to(torch.bfloat16) for _ in range(2)]
+q = torch.randn(1, 4, d, device="cuda").to(torch.bfloat16)
+table, free, none, some = i32([[0] * 96]), i32(list(range(20))), i32([0]), i32([n])
+def step():
+    s = mk.minisgl_build_slots(none, some, table, free, 4, 80, n)
+    mk.minisgl_store_kv_fp4(pool, 0, *kv, s.out_loc)
+    k, v = mk.minisgl_load_kv_fp4(pool, 0, table, s.seq_lens, s.q_offsets, n)
+    return k, v, mk.minisgl_decode_attn_fp4(pool, 0, q, table, s.seq_lens, 0.125)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = step()
+g.replay()
+torch.cuda.synchronize()
+got = [x.clone() for x in got]
+assert all(torch.equal(a, b) for a, b in zip(got, step())) and got[2].abs().max() > 0
+print("same")
+"""
+
+
+def test_first_use_may_be_captured():
+    """A new process whose first calls are captured, with no call before them."""
+    r = subprocess.run([sys.executable, "-c", FIRST_USE], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_binding_refusals():
