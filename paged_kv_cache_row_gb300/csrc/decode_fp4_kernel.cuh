@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
             issue(now_hb, now);
         }
         bool open = true, from_start = c.left == sch.len(c.r), live = false;
+        // which of its stream's partials the range begins with (later streams begin here)
+        int split = from_start ? 0 : seg - sch.range_of(sch.before(c.r, c.hb));
         int head = 0;
         for (; use > 0; --use) {
             if (open) {
@@ -304,13 +306,12 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
             if (c.left <= 0 || use == 1) {  // end of the stream or of the range
                 const bool last = c.left <= 0;
                 if (!MULTI || live) {
-                    const bool whole = from_start && last;
-                    const int split = whole ? 0 : seg - sch.range_of(sch.before(c.r, c.hb));
-                    w.close(a, (int64_t)c.r * Hq + head * G, G, whole, split, out_scale, lane);
+                    w.close(a, (int64_t)c.r * Hq + head * G, G, from_start && last, split, out_scale, lane);
                     if (last && lane == 0 && !sch.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
                 }
                 if (use > 1) sch.next_stream(c);
                 open = from_start = true;
+                split = 0;
             }
         }
     }
