@@ -408,9 +408,10 @@ struct Schedule {
             return;
         }
         // every thread sums the tiles of its chunks, then a scan over the CTA
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         __shared__ int s_sum[32], s_max[32];
         const int share = (chunks + blockDim.x - 1) / blockDim.x;
+        const int busy = (chunks + 32 * share - 1) / (32 * share);  // warps that have any
         const int k0 = min(tid * share, chunks), k1 = min(k0 + share, chunks);
         int mine = 0, mx = 0;
         for (int k = k0; k < k1; ++k) {
@@ -431,40 +432,53 @@ struct Schedule {
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 31) {
-            s_sum[warp] = inc;
-            s_max[warp] = mx;
-        }
-        __syncthreads();
-        int at = inc - mine;  // tiles before this thread's chunks
-        for (int w = 0; w < warp; ++w) at += s_sum[w];
-        for (int k = k0; k < k1; ++k) {
-            s_prefix[k] = at;
-            if (share == 1) break;
-            int nt[CHUNK];
-            chunk_tiles(k, nt);
-#pragma unroll
-            for (int q = 0; q < CHUNK; ++q) at += nt[q] * hblocks;
-        }
-        if (tid == 0) {
-            int all = 0, longest = 0;
-            for (int w = 0; w < warps; ++w) {
-                all += s_sum[w];
-                longest = max(longest, s_max[w]);
+        if (chunks <= 32) {  // warp 0 has them all
+            if (warp == 0 && lane < chunks) s_prefix[lane] = inc - mine;
+            if (tid == 31) {
+                s_prefix[chunks] = inc;
+                s_prefix[chunks + 1] = mx;
             }
-            s_prefix[chunks] = all;
-            s_prefix[chunks + 1] = longest;
+        } else {
+            if (lane == 31) {
+                s_sum[warp] = inc;
+                s_max[warp] = mx;
+            }
+            __syncthreads();
+            int at = inc - mine;  // tiles before this thread's chunks
+            for (int w = 0; w < min(warp, busy); ++w) at += s_sum[w];
+            for (int k = k0; k < k1; ++k) {
+                s_prefix[k] = at;
+                if (share == 1) break;
+                int nt[CHUNK];
+                chunk_tiles(k, nt);
+#pragma unroll
+                for (int q = 0; q < CHUNK; ++q) at += nt[q] * hblocks;
+            }
+            if (tid == 0) {
+                int all = 0, longest = 0;
+                for (int w = 0; w < busy; ++w) {
+                    all += s_sum[w];
+                    longest = max(longest, s_max[w]);
+                }
+                s_prefix[chunks] = all;
+                s_prefix[chunks + 1] = longest;
+            }
         }
         __syncthreads();
         total = s_prefix[chunks];
         // nseg ranges of L = total / nseg >= 1 tiles, the first `more` with one
         // more.  A stream of nt tiles meets at most (nt - 2) / L + 2 of them, and
         // L >= (nt - 1) / (max_splits - 1) keeps that within max_splits.
-        int want = a.split_tokens > 0 ? (int)(((int64_t)a.split_tokens + TILE - 1) / TILE) : 1;
-        want = max(want, (s_prefix[chunks + 1] + a.max_splits - 2) / (a.max_splits - 1));
-        const int most = total / want;
-        nseg = max(1, a.split_tokens > 0 ? most : min(ranges, most));
-        each = total / nseg;
+        const int longest = s_prefix[chunks + 1];
+        nseg = ranges;
+        each = (uint32_t)total / (uint32_t)ranges;
+        if (a.split_tokens > 0 || each == 0 || (int64_t)each * (a.max_splits - 1) < longest) {
+            int want = a.split_tokens > 0 ? (int)(((int64_t)a.split_tokens + TILE - 1) / TILE) : 1;
+            want = max(want, (longest + a.max_splits - 2) / (a.max_splits - 1));
+            const int most = total / want;
+            nseg = max(1, a.split_tokens > 0 ? most : min(ranges, most));
+            each = total / nseg;
+        }
         more = total - each * nseg;
     }
     __device__ __forceinline__ int begin(int seg) const { return seg * each + min(seg, more); }
@@ -507,7 +521,7 @@ struct Schedule {
                 q = i;
             }
         c.r = lo * CHUNK + q;
-        c.hb = off / n;
+        c.hb = hblocks == 1 ? 0 : off / n;
         c.left = len(c.r) - (off - c.hb * n) * TILE;
     }
     // Tiles of range seg.
@@ -517,7 +531,7 @@ struct Schedule {
     // The same, and its first tile (with no tiles: the stream).
     __device__ __forceinline__ int range(int seg, Cursor &c) const {
         if (whole) {
-            c.r = seg / hblocks;
+            c.r = hblocks == 1 ? seg : seg / hblocks;
             c.hb = seg - c.r * hblocks;
             c.left = len(c.r);
             return (c.left + TILE - 1) / TILE;

@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     pdl_wait();
     pdl_launch_dependents();
     Schedule sch;
-    sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int)gridDim.x * lay.subs, lay.whole);
+    sch.init(reinterpret_cast<int32_t *>(smem), a, MULTI ? lay.hblocks : 1, (int)gridDim.x * lay.subs, lay.whole);
     if (sch.total == 0) return;
 
     // warp (sub, head): the ring of its group
