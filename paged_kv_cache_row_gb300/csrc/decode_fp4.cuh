@@ -176,16 +176,31 @@ struct Stream {
             for (int n = 0; n < NG; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
     }
 
-    // The weights of 32 tokens, the first `left` of which count, as the B
-    // operand of the product with V.  k, sk: shared addresses of this head's K
-    // row and K scales in slot 0.
-    __device__ __forceinline__ void scores(uint32_t k, uint32_t sk, int stride, int left, int lane,
-                                           uint32_t (&pb)[2][NG][2]) {
+    // Where the lane reads in a stage (kp, skp of scores(), vp[2], svp[2] of
+    // values()), kept in registers: made again for every tile they took 17 of
+    // 634 instructions.  k, sk, v, sv: shared addresses of this head's K row, K
+    // scales, V row and V scales in slot 0.
+    __device__ __forceinline__ void addresses(uint32_t k, uint32_t sk, uint32_t v, uint32_t sv, int stride, int lane,
+                                              uint32_t (&rd)[6]) const {
         const int lg = lane >> 2, lt = lane & 3;
+        rd[0] = k + slot(lg) * stride + lt * (C::QPT / 2);
+        rd[1] = sk + slot(lg) * stride + (D == 128 ? 2 * lt : lt);
+        const uint32_t vo = lg * (C::OPT / 2), so = D == 128 ? lg : lg >> 1;
+        rd[2] = v + lt * stride + vo;
+        rd[3] = v + (4 + (lt ^ 2)) * stride + vo;
+        rd[4] = sv + lt * stride + so;
+        rd[5] = sv + (4 + (lt ^ 2)) * stride + so;
+#pragma unroll
+        for (int i = 0; i < 6; ++i) asm("" : "+r"(rd[i]));
+    }
+
+    // The weights of 32 tokens, the first `left` of which count, as the B
+    // operand of the product with V.
+    __device__ __forceinline__ void scores(uint32_t kp, uint32_t skp, int stride, int left, int lane,
+                                           uint32_t (&pb)[2][NG][2]) {
+        const int lg = lane >> 2;
         // ---- S^T = K Q^T for two blocks of 16 tokens ----
         float sa[2][NG][4];
-        const uint32_t kp = k + slot(lg) * stride + lt * (C::QPT / 2);
-        const uint32_t skp = sk + slot(lg) * stride + (D == 128 ? 2 * lt : lt);
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             constexpr int WORDS = C::QPT / 8;  // 32-bit words of a lane's channels
@@ -288,14 +303,11 @@ struct Stream {
         }
     }
 
-    // O^T += V^T P^T for the same tokens; v, sv: this head's V row and V scales in slot 0.
-    __device__ __forceinline__ void values(uint32_t v, uint32_t sv, int stride, int lane,
+    // O^T += V^T P^T for the same tokens.
+    __device__ __forceinline__ void values(uint32_t vp0, uint32_t vp1, uint32_t svp0, uint32_t svp1, int stride,
                                            const uint32_t (&pb)[2][NG][2]) {
-        const int lg = lane >> 2, lt = lane & 3;
         // tokens 2lt, 2lt+1, 2lt+8, 2lt+9 of a block: slots lt, 4 + (lt ^ 2), and 8 more
-        const uint32_t vo = lg * (C::OPT / 2), so = D == 128 ? lg : lg >> 1;
-        const uint32_t vp[2] = {v + lt * stride + vo, v + (4 + (lt ^ 2)) * stride + vo};
-        const uint32_t svp[2] = {sv + lt * stride + so, sv + (4 + (lt ^ 2)) * stride + so};
+        const uint32_t vp[2] = {vp0, vp1}, svp[2] = {svp0, svp1};
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
             constexpr int WORDS = C::OPT / 8;

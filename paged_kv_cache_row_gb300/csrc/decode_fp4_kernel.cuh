@@ -100,6 +100,12 @@ template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
+// base + row * stride, one multiply-add for each of K and V instead of a product and two sums
+__device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t row, uint32_t stride) {
+    const uint8_t *p;
+    asm("mad.wide.u32 %0, %1, %2, %3;\n" : "=l"(p) : "r"(row), "r"(stride), "l"(base));
+    return p;
+}
 // One arrival on `bar` when this thread's cp.async copies so far have landed.
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
@@ -179,10 +185,15 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     int in_hb = 0;
     bool have = off < HEADS * C::RB, shave = soff < HEADS * C::SB;  // the first block is full
 
+    // the lane's first destinations in stage 0, kept in registers as the sources are
+    uint32_t to_data = ring + slot_of(sub_tok) * stride + piece * 16;
+    uint32_t to_scale = ring + slot_of(ssub_tok) * stride + sk_off + sp * WIDE;
+    asm("" : "+r"(to_data), "+r"(to_scale));
+    asm("" : "+l"(ksrc), "+l"(vsrc), "+l"(ssrc));
     uint32_t in_at = 0, in_parity = 1;  // stage to fill; the first round finds every stage empty
     auto issue = [&](int hb, int raw) {
         const int row = min(max(raw, 0), a.num_rows - 1);
-        const uint32_t bar = bars + in_at * 16u, dst = ring + in_at * stage_bytes;
+        const uint32_t bar = bars + in_at * 16u, at_stage = in_at * stage_bytes;
         if (MULTI && hb != in_hb) {
             const int d = (hb - in_hb) * HEADS, nh = min(HEADS, Hkv - hb * HEADS);
             ksrc += d * C::RB;
@@ -196,27 +207,29 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
 #pragma unroll
         for (int i0 = 0; i0 < MOST; i0 += TOKS) {
             const int i = i0 + sub_tok;
-            const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i & 31) * data_stride;
-            const uint32_t to = dst + slot_of(i) * stride + piece * 16;
+            const uint32_t e = __shfl_sync(0xffffffffu, row, i & 31);
+            // (8 heads: slot_of() is linear in i)
+            const uint32_t to = to_data + at_stage +
+                                (HEADS == 8 ? slot_of(i0) - slot_of(0) : slot_of(i) - slot_of(sub_tok)) * stride;
             if (i < mine && have) {
-                cp_async_16(to, ksrc + e, 16);
-                if constexpr (TWO) cp_async_16(to + HALF * 16, vsrc + e, 16);
+                cp_async_16(to, row_at(ksrc, e, data_stride), 16);
+                if constexpr (TWO) cp_async_16(to + HALF * 16, row_at(vsrc, e, data_stride), 16);
             }
         }
 #pragma unroll
         for (int i0 = 0; i0 < MOST; i0 += STOKS) {
             const int i = i0 + ssub_tok;
-            const uint64_t e = (uint64_t)(uint32_t)__shfl_sync(0xffffffffu, row, i & 31) * scale_stride;
-            const uint32_t to = dst + slot_of(i) * stride + sk_off + sp * WIDE;
+            const uint8_t *from = row_at(ssrc, __shfl_sync(0xffffffffu, row, i & 31), scale_stride);
+            const uint32_t to = to_scale + at_stage + (slot_of(i) - slot_of(ssub_tok)) * stride;
             if (i < mine && shave) {
                 if constexpr (WIDE == 16) {
                     if (narrow) {  // rows that do not start on 16 bytes: d/16 bytes at a time
-                        for (int k = 0; k < 16; k += C::SB) cp_async_small<C::SB>(to + k, ssrc + e + k);
+                        for (int k = 0; k < 16; k += C::SB) cp_async_small<C::SB>(to + k, from + k);
                     } else {
-                        cp_async_16(to, ssrc + e, 16);
+                        cp_async_16(to, from, 16);
                     }
                 } else {
-                    cp_async_small<WIDE>(to, ssrc + e);
+                    cp_async_small<WIDE>(to, from);
                 }
             }
         }
@@ -230,6 +243,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     fp4::Stream<D, NG> w;
     uint32_t at = 0, parity = 0;  // stage to use
     const uint32_t my_k = ring + head_in * C::RB, my_s = ring + sk_off + head_in * C::SB;
+    uint32_t rd[6];  // where the lane reads in the first stage
+    w.addresses(my_k, my_s, my_k + v_off, my_s + (sv_off - sk_off), stride, lane, rd);
     const int seg_step = (int)gridDim.x * lay.subs;
     // neighbouring ranges on different SMs: few ranges spread over all of them
     for (int seg = blockIdx.x + sub * (int)gridDim.x; seg < sch.nseg; seg += seg_step) {
@@ -243,76 +258,73 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
                           make_uint4(0u, 0u, 0u, 0u));
             continue;
         }
+        // The tiles to fetch are those of pc until left reaches `stop`, then
+        // `later` more of the streams behind it.
         pc = c;
-        auto set_table = [&]() { table = a.page_table + (int64_t)pc.r * a.pt_stride + (sch.len(pc.r) - pc.left); };
-        auto fetch_next = [&]() {  // only called when a next tile exists
+        int stop, later = use;
+        auto enter = [&]() {
+            table = a.page_table + (int64_t)pc.r * a.pt_stride + (sch.len(pc.r) - pc.left);
+            const int n = min(later, (pc.left + TILE - 1) / TILE);
+            stop = pc.left - n * TILE;
+            later -= n;
+        };
+        auto advance = [&]() -> int {  // the next tile to fetch; its page-table entry
             pc.left -= TILE;
             table += TILE;
-            if (pc.left <= 0) {
+            if (pc.left <= stop && later > 0) {
                 sch.next_stream(pc);
-                set_table();
+                enter();
                 // its queries, wanted when this tile is used (67 -> 64 us at 1000 requests of 17 to 300 tokens)
                 w.prefetch(a, (int64_t)pc.r * Hq + (MULTI ? pc.hb * HEADS + head_in : head_in) * G, G,
                            !MULTI || pc.hb * HEADS + head_in < Hkv, lane);
             }
+            return pc.left > stop ? load_row(pc.left) : 0;
         };
-        set_table();
-        int todo = use;  // tiles not asked for yet
+        enter();
         // the first two tiles' page-table entries at once, then one tile ahead
-        int row = load_row(pc.left), hb = pc.hb;
-        for (int i = 0; i < stages - 1 && todo > 0; ++i) {
-            const int now = row, now_hb = hb;
-            if (--todo > 0) {
-                fetch_next();
-                row = load_row(pc.left);
-                hb = pc.hb;
-            }
+        int row = load_row(pc.left);
+        for (int i = 0; i < stages - 1 && pc.left > stop; ++i) {
+            const int now = row, now_hb = pc.hb;
+            row = advance();
             issue(now_hb, now);
         }
-        bool open = true, from_start = c.left == sch.len(c.r), live = false;
+        bool from_start = c.left == sch.len(c.r);
         // which of its stream's partials the range begins with (later streams begin here)
         int split = from_start ? 0 : seg - sch.range_of(sch.before(c.r, c.hb));
-        int head = 0;
-        for (; use > 0; --use) {
-            if (open) {
-                open = false;
-                head = MULTI ? c.hb * HEADS + head_in : head_in;
-                live = !MULTI || head < Hkv;
-                w.open(live ? static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)c.r * Hq + head * G) * D : nullptr, G,
-                       scale_log2, lane);
-            }
-            guarded_wait(bars + at * 16u, parity, &s_abort);
-            const uint32_t st = at * stage_bytes;
-            uint32_t pb[2][NG][2];
-            if (!MULTI || live) {
-                w.scores(my_k + st, my_s + st, stride, c.left, lane, pb);
-                w.values(my_k + st + v_off, my_s + st + (sv_off - sk_off), stride, lane, pb);
-            }
-            if (todo > 0) {
-                issue(hb, row);  // into the stage of the tile before this one
-                if (--todo > 0) {
-                    fetch_next();
-                    row = load_row(pc.left);  // for the next iteration
-                    hb = pc.hb;
+        while (use > 0) {  // a stream, or the range's part of it
+            const int head = MULTI ? c.hb * HEADS + head_in : head_in;
+            const bool live = !MULTI || head < Hkv;
+            w.open(live ? static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)c.r * Hq + head * G) * D : nullptr, G,
+                   scale_log2, lane);
+            const int n = min(use, (c.left + TILE - 1) / TILE), end = c.left - n * TILE;
+            use -= n;
+            for (; c.left > end; c.left -= TILE) {
+                guarded_wait(bars + at * 16u, parity, &s_abort);
+                const uint32_t st = at * stage_bytes;
+                uint32_t pb[2][NG][2];
+                if (live) {
+                    w.scores(rd[0] + st, rd[1] + st, stride, c.left, lane, pb);
+                    w.values(rd[2] + st, rd[3] + st, rd[4] + st, rd[5] + st, stride, pb);
+                }
+                if (pc.left > stop) {  // into the stage of the tile before this one
+                    issue(pc.hb, row);
+                    row = advance();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + at * 16u + 8u);
+                if (++at == (uint32_t)stages) {
+                    at = 0;
+                    parity ^= 1;
                 }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars + at * 16u + 8u);
-            if (++at == (uint32_t)stages) {
-                at = 0;
-                parity ^= 1;
+            const bool last = c.left <= 0;
+            if (live) {
+                w.close(a, (int64_t)c.r * Hq + head * G, G, from_start && last, split, out_scale, lane);
+                if (last && lane == 0 && !sch.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
             }
-            c.left -= TILE;
-            if (c.left <= 0 || use == 1) {  // end of the stream or of the range
-                const bool last = c.left <= 0;
-                if (!MULTI || live) {
-                    w.close(a, (int64_t)c.r * Hq + head * G, G, from_start && last, split, out_scale, lane);
-                    if (last && lane == 0 && !sch.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
-                }
-                if (use > 1) sch.next_stream(c);
-                open = from_start = true;
-                split = 0;
-            }
+            if (use > 0) sch.next_stream(c);
+            from_start = true;
+            split = 0;
         }
     }
     cp_async_wait<0>();  // nothing in flight when the CTA ends, even after a wait that ran out
