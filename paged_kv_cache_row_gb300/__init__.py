@@ -660,7 +660,9 @@ class KVPoolFP4:
     The rows of a layer are contiguous (H_kv, ..); the axes before them may have
     any strides.  k_exp, v_exp: the power of two that K and V values are
     multiplied with, one int or one per layer.  Caller-owned device memory; a
-    new pool's bytes should be zero (KVPoolFP4.zeros makes one)."""
+    new pool's bytes should be zero (KVPoolFP4.zeros makes one).  With one KV
+    head use pages of 16 rows or more: a row's 64 and 8 bytes from anywhere take
+    twice as long to read as when their neighbours are used too."""
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, page_size: int = 1,
                  k_exp: Union[int, Sequence[int]] = 0, v_exp: Union[int, Sequence[int]] = 0):

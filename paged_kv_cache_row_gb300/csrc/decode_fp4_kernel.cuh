@@ -24,21 +24,24 @@
 // token's K row of eight heads (512 bytes at d 128), so few rows and lines are
 // touched at a time.  Page-table entries are read a tile before the rows they
 // name, and not looked at until then (a clamp right behind the load held its
-// warp for the load's latency once per tile: 174 us where 154 are taken now).
+// warp for the load's latency once per tile: 174 us where 156 were taken then).
 // Rows past a request's end repeat its last row; their weights are zero.
 //
 // Measured (8 KV heads, d 128, warm): 256 requests of 1k to 8k tokens in
-// single-row pages 154 us, 5.2 TB/s of algorithmic bytes; 32 of 8k to 32k in
-// 64-row pages 145 us.  With the arithmetic left out 151 and 135, with the
-// loads left out 129 and 124: the two nearly balance, and about 10 us are the
-// start of the pipeline, the last ranges and the merge.
+// single-row pages 149 us, 5.4 TB/s of algorithmic bytes; 32 of 8k to 32k in
+// 64-row pages 139 us.  With the arithmetic left out 141 and 124, with the
+// loads left out 138 and 130: the two nearly balance, so that every instruction
+// of a tile counts (634 to 598 a warp took 152 and 143.5 us to these), and about
+// 10 us are the start of the pipeline, the last ranges and the merge.
 //
 // Arrangements timed and not kept, on the first of these: every warp fetching
 // its own head's 64- and 8-byte pieces 241 us; one CTA barrier per tile for
 // the mbarriers 204 (174 then); one bulk copy (TMA) per row 396, about 41
 // cycles a copy and SM, whatever its size; four producer warps with eight
 // consumers and six stages 164, with sixteen consumers and registers shared
-// out 151, but 1.5 to 2.5 times slower at 1 and 2 heads.
+// out 151, but 1.5 to 2.5 times slower at 1 and 2 heads.  At 149: rows marked to
+// be evicted first 153, two accumulators for Q K^T 150, its two blocks of 16
+// tokens interleaved 152, the mbarriers inside the stages 151.
 #pragma once
 #include <algorithm>
 #include <cmath>
@@ -339,9 +342,9 @@ namespace {
 // What bounds it are rounds of dependent loads, about 1 us each behind the
 // launch, and how many rows are under way.  There are two rounds: the length
 // and the count, then the LSEs and MOST partials.  MOST 16 takes 96 registers
-// and so 2432 rows at once, MOST 4 takes 40 and three times as many: the decode
-// of 1024 rows in 2-3 partials takes 44.6 / 45.5 us, of 2048 rows in about 10
-// 145.4 / 146.9, of 8192 rows in 2-3 156.6 / 153.9.
+// and so 2432 rows at once, MOST 4 takes 40 and three times as many: 16 takes
+// 0.9 us less for 1024 rows in 2-3 partials, 1.5 less for 2048 rows in about 10,
+// 2.7 more for 8192 rows in 2-3.
 template <int D, int MOST>
 __global__ void __launch_bounds__(128, MOST > 8 ? 4 : 12) decode_fp4_merge_kernel(const DecodeArgs a) {
     constexpr int CPL = D / 32;  // channels per lane
