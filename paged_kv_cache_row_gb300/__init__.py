@@ -615,6 +615,9 @@ def _on(stream, index: int):
     return torch.cuda.stream(stream)
 
 
+_I32, _BF16 = torch.int32, torch.bfloat16
+
+
 def _at(t: torch.Tensor, name: str, dtype: torch.dtype, index: Optional[int] = None) -> int:
     """The CUDA device index of t, a tensor of this type (on device `index` if given)."""
     i = t.get_device()
@@ -625,16 +628,19 @@ def _at(t: torch.Tensor, name: str, dtype: torch.dtype, index: Optional[int] = N
     return i
 
 
-def _vec(t: torch.Tensor, name: str, n: Optional[int] = None, index: Optional[int] = None) -> int:
-    i = _at(t, name, torch.int32, index)
+# The checks below look at a tensor themselves and leave it to _at to say what
+# is wrong: a call less for each argument.
+def _vec(t: torch.Tensor, name: str, n: Optional[int], index: int) -> None:
+    if t.get_device() != index or t.dtype is not _I32:
+        _at(t, name, _I32, index)
     if (n is not None and t.numel() != n) or not t.is_contiguous():
         raise MinisglError(f"{name} must be a contiguous int32 tensor" + (f" of {n} elements" if n is not None else ""))
-    return i
 
 
-def _table(t: torch.Tensor, n: int, index: Optional[int] = None) -> Tuple[int, int]:
+def _table(t: torch.Tensor, n: int, index: int) -> Tuple[int, int]:
     """Row stride and width of a page table of n rows."""
-    _at(t, "page_table", torch.int32, index)
+    if t.get_device() != index or t.dtype is not _I32:
+        _at(t, "page_table", _I32, index)
     shape, strides = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != n or (shape[1] > 1 and strides[1] != 1):
         raise MinisglError("page_table must be [B, W] with unit column stride")
@@ -644,7 +650,8 @@ def _table(t: torch.Tensor, n: int, index: Optional[int] = None) -> Tuple[int, i
 
 def _kv_rows(t: torch.Tensor, name: str, n: int, row: int, index: int, what: str = "n_tokens") -> int:
     """Token stride of n contiguous rows of `row` bf16 elements."""
-    _at(t, name, torch.bfloat16, index)
+    if t.get_device() != index or t.dtype is not _BF16:
+        _at(t, name, _BF16, index)
     shape, strides = t.shape, t.stride()
     usual = (len(shape) == 3 and shape[0] == n and shape[1] * shape[2] == row and strides[2] == 1
              and strides[1] == shape[2])
@@ -747,11 +754,12 @@ def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, pa
     B, total = cached_lens.numel(), int(total_tokens)
     if total < 0:
         raise MinisglError("total_tokens must not be negative")
-    dev = _vec(cached_lens, "cached_lens")
+    dev = _at(cached_lens, "cached_lens", _I32)
     if stream is not None or _device() != dev:
         with _on(stream, dev):
             return minisgl_build_slots(cached_lens, extend_lens, page_table, free_pages, page_size, dummy_row,
                                        total, out)
+    _vec(cached_lens, "cached_lens", None, dev)
     _vec(extend_lens, "extend_lens", B, dev)
     _vec(free_pages, "free_pages", None, dev)
     stride, width = _table(page_table, B, dev)
@@ -759,9 +767,9 @@ def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, pa
         for t, nm, n in zip(out, Slots._fields, (total, total, B + 1, B, 1)):
             _vec(t, nm, n, dev)
     else:
-        i32, one = torch.int32, (1,)
-        out = Slots(_new((total,), one, i32), _new((total,), one, i32), _new((B + 1,), one, i32),
-                    _new((B,), one, i32), _new(one, one, i32))
+        one = (1,)
+        out = Slots(_new((total,), one, _I32), _new((total,), one, _I32), _new((B + 1,), one, _I32),
+                    _new((B,), one, _I32), _new(one, one, _I32))
     loc, pos, off, lens, used = out
     _check(load_library().minisgl_build_slots(
         cached_lens.data_ptr(), extend_lens.data_ptr(), B, page_table.data_ptr(), stride, width,
@@ -805,9 +813,9 @@ def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, l
     ks = row if k_out is None else _kv_rows(k_out, "k_out", total, row, dev, "total_tokens")
     vs = row if v_out is None else _kv_rows(v_out, "v_out", total, row, dev, "total_tokens")
     if k_out is None:
-        k_out = _new((total, H, d), (row, d, 1), torch.bfloat16)
+        k_out = _new((total, H, d), (row, d, 1), _BF16)
     if v_out is None:
-        v_out = _new((total, H, d), (row, d, 1), torch.bfloat16)
+        v_out = _new((total, H, d), (row, d, 1), _BF16)
     _check(load_library().minisgl_load_kv_fp4(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
                                               lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
                                               v_out.data_ptr(), ks, vs, _raw_stream(dev)), "load_kv_fp4")
@@ -827,7 +835,7 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
                             max_splits: int = 32, stream=None) -> torch.Tensor:
     """Decode attention of q [B, H_q, d] over each request's page_table row of
     the 4-bit pool.  Without a workspace the call allocates its own."""
-    dev = _at(q, "q", torch.bfloat16, pool._index)
+    dev = _at(q, "q", _BF16, pool._index)
     if stream is not None or _device() != dev:
         with _on(stream, dev):
             return minisgl_decode_attn_fp4(pool, layer, q, page_table, seq_lens, sm_scale, out, workspace,
@@ -839,9 +847,9 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
     stride, width = _table(page_table, B, dev)
     _vec(seq_lens, "seq_lens", B, dev)
     if out is None:
-        out = _new((B, Hq, d), (Hq * d, d, 1), torch.bfloat16)
+        out = _new((B, Hq, d), (Hq * d, d, 1), _BF16)
     else:
-        _at(out, "out", torch.bfloat16, dev)
+        _at(out, "out", _BF16, dev)
         if out.shape != shape or not out.is_contiguous():
             raise MinisglError("out must be contiguous with the shape of q")
     if workspace is None:
