@@ -207,18 +207,13 @@ struct Stream {
             uint32_t k0[WORDS], k1[WORDS];
             lds_words<WORDS>(kp + (16 * b) * stride, k0);
             lds_words<WORDS>(kp + (16 * b + 8) * stride, k1);
-            uint32_t s0[2], s1[2];  // the scales of the lane's one or two blocks, in both halves
+            uint32_t s0, s1;  // the scales of the lane's two blocks, or of its one (twice)
             if constexpr (D == 128) {
-                const uint32_t h0 = e4m3x2_to_f16x2(lds_u16(skp + (16 * b) * stride));
-                const uint32_t h1 = e4m3x2_to_f16x2(lds_u16(skp + (16 * b + 8) * stride));
-                s0[0] = __byte_perm(h0, h0, 0x1010);
-                s0[1] = __byte_perm(h0, h0, 0x3232);
-                s1[0] = __byte_perm(h1, h1, 0x1010);
-                s1[1] = __byte_perm(h1, h1, 0x3232);
+                s0 = e4m3x2_to_f16x2(lds_u16(skp + (16 * b) * stride));
+                s1 = e4m3x2_to_f16x2(lds_u16(skp + (16 * b + 8) * stride));
             } else {
-                const uint32_t h0 = lds_u8(skp + (16 * b) * stride), h1 = lds_u8(skp + (16 * b + 8) * stride);
-                s0[0] = s0[1] = e4m3x2_to_f16x2(h0 | (h0 << 8));
-                s1[0] = s1[1] = e4m3x2_to_f16x2(h1 | (h1 << 8));
+                s0 = e4m3x2_to_f16x2(lds_u8(skp + (16 * b) * stride));
+                s1 = e4m3x2_to_f16x2(lds_u8(skp + (16 * b + 8) * stride));
             }
 #pragma unroll
             for (int i = 0; i < WORDS; ++i) {
@@ -227,8 +222,8 @@ struct Stream {
                 e2m1x8_to_f16x2(k1[i], e1);
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    e0[u] = mul_f16x2(e0[u], s0[i / 2]);
-                    e1[u] = mul_f16x2(e1[u], s1[i / 2]);
+                    e0[u] = i < 2 ? mul_f16x2_half<false>(e0[u], s0) : mul_f16x2_half<true>(e0[u], s0);
+                    e1[u] = i < 2 ? mul_f16x2_half<false>(e1[u], s1) : mul_f16x2_half<true>(e1[u], s1);
                 }
 #pragma unroll
                 for (int n = 0; n < NG; ++n) {

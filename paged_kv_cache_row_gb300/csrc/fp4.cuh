@@ -54,6 +54,20 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     return c;
 }
 
+// a times one half of b, the low or the high (the multiplication can take either
+// half twice, so that no permutation is needed first)
+template <bool HIGH>
+__device__ __forceinline__ uint32_t mul_f16x2_half(uint32_t a, uint32_t b) {
+    uint32_t c;
+    if constexpr (HIGH)
+        asm("{\n .reg .b16 l, h;\n .reg .b32 s;\n mov.b32 {l, h}, %2;\n mov.b32 s, {h, h};\n"
+            " mul.rn.f16x2 %0, %1, s;\n}\n" : "=r"(c) : "r"(a), "r"(b));
+    else
+        asm("{\n .reg .b16 l, h;\n .reg .b32 s;\n mov.b32 {l, h}, %2;\n mov.b32 s, {l, l};\n"
+            " mul.rn.f16x2 %0, %1, s;\n}\n" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t h) {
     float2 f;
     asm("{\n .reg .f16 l, u;\n mov.b32 {l, u}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, u;\n}\n"
