@@ -178,7 +178,7 @@ struct Stream {
 
     // Where the lane reads in a stage (kp, skp of scores(), vp[2], svp[2] of
     // values()), kept in registers: made again for every tile they took 17 of
-    // 634 instructions.  k, sk, v, sv: shared addresses of this head's K row, K
+    // 634 instructions a tile.  k, sk, v, sv: shared addresses of this head's K row, K
     // scales, V row and V scales in slot 0.
     __device__ __forceinline__ void addresses(uint32_t k, uint32_t sk, uint32_t v, uint32_t sv, int stride, int lane,
                                               uint32_t (&rd)[6]) const {

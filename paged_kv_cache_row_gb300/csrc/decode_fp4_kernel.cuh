@@ -29,9 +29,9 @@
 //
 // Measured (8 KV heads, d 128, warm): 256 requests of 1k to 8k tokens in
 // single-row pages 149 us, 5.4 TB/s of algorithmic bytes; 32 of 8k to 32k in
-// 64-row pages 139 us.  With the arithmetic left out 141 and 124, with the
-// loads left out 138 and 130: the two nearly balance, so that every instruction
-// of a tile counts (634 to 598 a warp took 152 and 143.5 us to these), and about
+// 64-row pages 137 us.  With the arithmetic left out 144 and 127, with the
+// loads left out 137 and 129: the two nearly balance, so that every instruction
+// of a tile counts (634 to 588 a warp took 152 and 143.5 us to these), and about
 // 10 us are the start of the pipeline, the last ranges and the merge.
 //
 // Arrangements timed and not kept, on the first of these: every warp fetching
