@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "decode_fp4.cuh"
+#include "decode_fp4_plan.h"
 #include "tcgen05.cuh"
 
 namespace minisgl {
@@ -177,16 +178,19 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
     const bool is_v = !TWO && piece >= HALF;
     const int off = !TWO && piece >= PIECES ? 1 << 30 : (is_v ? piece - HALF : piece) * 16;
     const uint8_t *ksrc = (is_v ? pool.v_data : pool.k_data) + off, *vsrc = pool.v_data + off;
-    constexpr int WIDE = HEADS * C::SB % 16 == 0 ? 16 : C::SB;  // bytes of a scale piece
+    constexpr int WIDE = fp4::scale_piece(HEADS, C::SB);  // bytes of a scale piece
     const bool narrow = WIDE == 16 && !lay.wide_scales;
     constexpr int SHALF = HEADS * C::SB / WIDE, SPIECES = 2 * SHALF, SLP = log2_up(SPIECES), STOKS = 32 >> SLP;
     const int sp = lane & ((1 << SLP) - 1), ssub_tok = lane >> SLP;
     const bool s_is_v = sp >= SHALF;
     const int soff = sp >= SPIECES ? 1 << 30 : (s_is_v ? sp - SHALF : sp) * WIDE;
     const uint8_t *ssrc = (s_is_v ? pool.v_scale : pool.k_scale) + soff;
-    // the head block that the sources above belong to, and which of the lane's pieces it has
+    // the head block that the sources above belong to, whether it has the lane's
+    // data piece, and the bytes of the lane's scale piece in it (fewer than WIDE
+    // only in a short last block; the first block is full)
     int in_hb = 0;
-    bool have = off < HEADS * C::RB, shave = soff < HEADS * C::SB;  // the first block is full
+    bool have = off < HEADS * C::RB;
+    int sbytes = fp4::piece_bytes(HEADS * C::SB, soff, WIDE);
 
     // the lane's first destinations in stage 0, kept in registers as the sources are
     uint32_t to_data = ring + slot_of(sub_tok) * stride + piece * 16;
@@ -198,12 +202,12 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
         const int row = min(max(raw, 0), a.num_rows - 1);
         const uint32_t bar = bars + in_at * 16u, at_stage = in_at * stage_bytes;
         if (MULTI && hb != in_hb) {
-            const int d = (hb - in_hb) * HEADS, nh = min(HEADS, Hkv - hb * HEADS);
+            const int d = (hb - in_hb) * HEADS, nh = fp4::heads_of_block(Hkv, HEADS, hb);
             ksrc += d * C::RB;
             vsrc += d * C::RB;
             ssrc += d * C::SB;
             have = off < nh * C::RB;
-            shave = soff < nh * C::SB;
+            sbytes = fp4::piece_bytes(nh * C::SB, soff, WIDE);
             in_hb = hb;
         }
         guarded_wait(bar + 8u, in_parity, &s_abort);
@@ -224,12 +228,13 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
             const int i = i0 + ssub_tok;
             const uint8_t *from = row_at(ssrc, __shfl_sync(0xffffffffu, row, i & 31), scale_stride);
             const uint32_t to = to_scale + at_stage + (slot_of(i) - slot_of(ssub_tok)) * stride;
-            if (i < mine && shave) {
+            if (i < mine && sbytes > 0) {
                 if constexpr (WIDE == 16) {
+                    const int n = MULTI ? sbytes : 16;
                     if (narrow) {  // rows that do not start on 16 bytes: d/16 bytes at a time
-                        for (int k = 0; k < 16; k += C::SB) cp_async_small<C::SB>(to + k, from + k);
+                        for (int k = 0; k < n; k += C::SB) cp_async_small<C::SB>(to + k, from + k);
                     } else {
-                        cp_async_16(to, from, 16);
+                        cp_async_16(to, from, n);  // reads n bytes
                     }
                 } else {
                     cp_async_small<WIDE>(to, from);
@@ -478,11 +483,9 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
 
 }  // namespace
 
-// Head blocks of equal size, at most 8 heads (the last may be one short).
 template <int D, int NG>
 cudaError_t launch_decode_fp4_as(const DecodeFp4Args &a, cudaStream_t s) {
-    const int hblocks = (a.d.num_kv_heads + 7) / 8;
-    switch ((a.d.num_kv_heads + hblocks - 1) / hblocks) {
+    switch (fp4::block_heads(a.d.num_kv_heads)) {
         case 1: return launch_cfg<D, NG, 1>(a, s);
         case 2: return launch_cfg<D, NG, 2>(a, s);
         case 3: return launch_cfg<D, NG, 3>(a, s);

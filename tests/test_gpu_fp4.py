@@ -381,6 +381,27 @@ def test_scale_rows_that_start_anywhere(H, d):
         assert (np.abs(o.double().cpu().numpy() - want) <= bound).all()
 
 
+@pytest.mark.parametrize("slots", [0, 1, 4], ids=["packed", "one-more", "aligned"])
+@pytest.mark.parametrize("H,d", [(11, 128), (15, 64), (15, 128), (17, 128), (25, 64), (30, 64), (57, 128)])
+def test_decode_short_last_head_block(H, d, slots):
+    """Head counts whose last block has fewer heads than the others, up to the
+    pool's last row, with rows of scales that end with the pool's memory or
+    have room for more heads behind them."""
+    R, lens = 150, [150, 40]
+    room = -(-H // slots) * slots + (slots == 1) if slots else H
+    data = torch.zeros((2, 1, R, H, d // 2), dtype=torch.uint8, device=DEV)
+    scales = torch.full((2, 1, R, room, d // 16), 0x7F, dtype=torch.uint8, device=DEV)[:, :, :, :H]
+    pool = mk.KVPoolFP4(data, scales, k_exp=-2, v_exp=-1)
+    pool.data.random_(0, 256)
+    pool.scales.random_(0x18, 0x48)
+    pt = np.zeros((2, 160), dtype=int)
+    pt[0, :150] = np.random.default_rng(H).permutation(R)
+    pt[1, :40] = R - 1 - np.arange(40)
+    q = kv_like((2, 2 * H, d), 3).to(DEV)
+    check_decode(pool, q, pt, lens)
+    check_decode(pool, q, pt, lens, split_tokens=32)
+
+
 @pytest.mark.parametrize("split", [1, 32, 48, 100, 10 ** 6])
 @pytest.mark.parametrize("max_splits", [2, 5, 64, 256])
 def test_decode_split_counts(split, max_splits):
