@@ -40,15 +40,17 @@ __global__ void __launch_bounds__(SLOT_THREADS) build_slots_kernel(SlotArgs a, i
     auto page_of = [&](int p) { return shift >= 0 ? p >> shift : p / a.page_size; };
     // pages that cover the first p positions
     auto pages_for = [&](int p) { return page_of(p) + (p - page_of(p) * a.page_size ? 1 : 0); };
+    // No early start for the next kernel: the library's other kernels read the
+    // page table, out_loc, positions and lengths with non-coherent loads, whose
+    // memory must not change while they are resident.
     pdl_wait();
-    pdl_launch_dependents();
 
     // each thread sums `per` consecutive requests, then a block-wide scan
     const int per = (B + SLOT_THREADS - 1) / SLOT_THREADS;
     const int r0 = min(tid * per, B), r1 = min(r0 + per, B);
     int sum_e = 0, sum_p = 0;
     for (int r = r0; r < r1; ++r) {
-        const int c = min(__ldg(a.cached_lens + r), SLOT_SAT), e = min(max(__ldg(a.extend_lens + r), 0), SLOT_SAT);
+        const int c = min(a.cached_lens[r], SLOT_SAT), e = min(max(a.extend_lens[r], 0), SLOT_SAT);
         const int start = max(c, 0), end = min(sat_add(start, e), W);
         const int need = c < 0 ? 0 : max(pages_for(end) - pages_for(start), 0);
         // s_off, s_page hold each request's own numbers until the scan is known
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(SLOT_THREADS) build_slots_kernel(SlotArgs a, i
             if (i64 >= min(all, a.total_tokens)) continue;
             const int i = (int)i64;
             while (s_off[r + 1] <= i) ++r;
-            const int c = min(__ldg(a.cached_lens + r), SLOT_SAT), start = max(c, 0);
+            const int c = min(a.cached_lens[r], SLOT_SAT), start = max(c, 0);
             const int p = sat_add(start, i - s_off[r]);
             pos[u] = p;
             if (p >= W) continue;

@@ -139,7 +139,7 @@ struct Stream {
                 const __nv_bfloat16 *src = q + h * D + lt * C::QPT;
 #pragma unroll
                 for (int i = 0; i < C::QPT / 8; ++i) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + i);
+                    const uint4 v = reinterpret_cast<const uint4 *>(src)[i];
                     w[4 * i] = v.x;
                     w[4 * i + 1] = v.y;
                     w[4 * i + 2] = v.z;
@@ -494,12 +494,12 @@ struct Schedule {
         const int longer = more * (each + 1);  // tiles of the longer ranges
         return t < longer ? t / (each + 1) : more + (t - longer) / each;
     }
-    __device__ __forceinline__ int len(int r) const { return clamp_len(__ldg(seq_lens + r), W); }
+    __device__ __forceinline__ int len(int r) const { return clamp_len(seq_lens[r], W); }
     __device__ __forceinline__ int tiles(int r) const { return (len(r) + TILE - 1) / TILE; }
     // the same of a chunk's requests, all loads at once
     __device__ __forceinline__ void chunk_tiles(int k, int (&nt)[CHUNK]) const {
 #pragma unroll
-        for (int q = 0; q < CHUNK; ++q) nt[q] = k * CHUNK + q < batch ? __ldg(seq_lens + k * CHUNK + q) : 0;
+        for (int q = 0; q < CHUNK; ++q) nt[q] = k * CHUNK + q < batch ? seq_lens[k * CHUNK + q] : 0;
 #pragma unroll
         for (int q = 0; q < CHUNK; ++q) nt[q] = (clamp_len(nt[q], W) + TILE - 1) / TILE;
     }

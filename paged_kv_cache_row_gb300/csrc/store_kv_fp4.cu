@@ -38,15 +38,24 @@ constexpr int LOAD_TOKENS = 128; // most tokens of a load tile
 
 }  // namespace
 
+// Every load here is a coherent one: the kernel is resident while the one
+// before it may still write the slots, the new rows or the pool.
+__device__ __forceinline__ uint4 ld_v4(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
 // 32 bytes from 32-byte (WIDE) or 16-byte aligned memory
 template <bool WIDE>
 __device__ __forceinline__ void ld_32(const void *p, uint32_t (&x)[8]) {
     if constexpr (WIDE) {
-        asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
                      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7])
                      : "l"(p));
     } else {
-        const uint4 a = ld_nc_v4(p), b = ld_nc_v4(static_cast<const char *>(p) + 16);
+        const uint4 a = ld_v4(p), b = ld_v4(static_cast<const char *>(p) + 16);
         x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
     }
 }
@@ -116,7 +125,7 @@ __global__ void __launch_bounds__(MAX_THREADS, STORE_RESIDENT / MAX_THREADS) sto
             uint32_t x[8], sb;
             uint2 c;
             ld_32<WIDE>(src + i * tok_stride, x);
-            const int row = __ldg(a.out_loc + i);
+            const int row = a.out_loc[i];
             quantise16(x, unit, c, sb);
             // out-of-range rows are a caller error; clamp so the write stays in the pool
             const uint32_t r = (uint32_t)min(max(row, 0), a.pool.num_rows - 1);
@@ -148,16 +157,16 @@ __global__ void __launch_bounds__(MAX_THREADS, LOAD_RESIDENT / MAX_THREADS)
                 int lo = 0, hi = a.batch;  // the last request with offsets[r] <= t
                 while (hi - lo > 1) {
                     const int mid = (lo + hi) >> 1;
-                    if (__ldg(a.offsets + mid) <= t) lo = mid; else hi = mid;
+                    if (a.offsets[mid] <= t) lo = mid; else hi = mid;
                 }
                 req = lo;
             }
-            int end = __ldg(a.offsets + req + 1);
-            while (req + 1 < a.batch && end <= t) end = __ldg(a.offsets + ++req + 1);
-            const int64_t j = t - __ldg(a.offsets + req);
-            const int n = min(max(__ldg(a.lens + req), 0), a.pt_width);
+            int end = a.offsets[req + 1];
+            while (req + 1 < a.batch && end <= t) end = a.offsets[++req + 1];
+            const int64_t j = t - a.offsets[req];
+            const int n = min(max(a.lens[req], 0), a.pt_width);
             if (j >= 0 && j < n && t < end)
-                row = min(max(__ldg(a.page_table + req * a.pt_stride + j), 0), a.pool.num_rows - 1);
+                row = min(max(a.page_table[req * a.pt_stride + j], 0), a.pool.num_rows - 1);
         }
         rows[threadIdx.x] = row;
     };
@@ -187,8 +196,8 @@ __global__ void __launch_bounds__(MAX_THREADS, LOAD_RESIDENT / MAX_THREADS)
                     row[u] = i < tile_toks ? rows[i] : -1;
                     if (row[u] >= 0) {
                         const uint32_t r = (uint32_t)row[u];
-                        c[u] = __ldg(reinterpret_cast<const uint2 *>(data + (uint64_t)r * (uint32_t)a.pool.data_stride));
-                        sb[u] = __ldg(scale + (uint64_t)r * (uint32_t)a.pool.scale_stride);
+                        c[u] = *reinterpret_cast<const uint2 *>(data + (uint64_t)r * (uint32_t)a.pool.data_stride);
+                        sb[u] = scale[(uint64_t)r * (uint32_t)a.pool.scale_stride];
                     }
                 }
 #pragma unroll

@@ -2,6 +2,8 @@
 torch's formats and closed forms, and the calls' refusals (checked on the host
 before any device work; the pointers are never dereferenced)."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -186,3 +188,27 @@ def test_binding_refuses_host_tensors(lib):
 def test_pool_bytes():
     assert mk.kv_pool_fp4_bytes(32, 8, 128, 1000) == 2 * 32 * 8 * 72 * 1000
     assert mk.kv_pool_bytes(32, 8, 128, 1000) / mk.kv_pool_fp4_bytes(32, 8, 128, 1000) == 256 / 72
+
+
+def _code(name):
+    """A CUDA source without its comments."""
+    path = os.path.join(os.path.dirname(os.path.abspath(mk.__file__)), "csrc", name)
+    return re.sub(r"//[^\n]*|/\*.*?\*/", "", open(path).read(), flags=re.S)
+
+
+SOURCES = ["build_slots.cu", "store_kv_fp4.cu", "fp4.cuh", "decode_fp4.cu", "decode_fp4.cuh", "decode_fp4_kernel.cuh"]
+
+
+@pytest.mark.parametrize("name", SOURCES)
+def test_early_started_kernels_load_coherently(name):
+    """These kernels are resident while the one before them may still write
+    what they read (lengths, slots, new rows, the pool): a non-coherent load
+    wants memory that does not change for the kernel's whole life."""
+    assert not re.findall(r"__ldg|ld_nc\w*|\.global\.nc", _code(name))
+
+
+def test_slots_start_no_kernel_early():
+    """The older kernels read page_table, out_loc and lengths with non-coherent
+    loads, so they must not be resident while build_slots writes them."""
+    code = _code("build_slots.cu")
+    assert "pdl_wait()" in code and "pdl_launch_dependents" not in code
