@@ -434,7 +434,8 @@ int minisgl_check_shared_prefix(const int32_t *page_table, int32_t batch, int64_
  * request owns ceil(C / page_size) of them, its last cached token's row being
  * page_table[r, C-1].  With first(r) = the new pages of requests 0 .. r-1 and
  * S = min(C + E, pt_width):
- *   row(r, p) = page_table[r, C-1] + p - (C-1)          p in the page of C-1,
+ *   row(r, p) = page_table[r, C-1] + p - (C-1)          p in the page of C-1
+ *                 (dummy_row if page_table[r, C-1] is dummy_row),
  *               free_pages[first(r) + p/page_size - ceil(C/page_size)] * page_size
  *                 + p % page_size                        otherwise;
  *   page_table[r, p] = row(r, p),  C <= p < S (other entries are not written);
@@ -447,7 +448,10 @@ int minisgl_check_shared_prefix(const int32_t *page_table, int32_t batch, int64_
  * num_free free pages (pages_used > num_free then: the caller reads
  * pages_used after the stream and frees pages or shortens the batch), and
  * fills out_loc from q_offsets[batch] to total_tokens (with position 0), so
- * that a captured step of total_tokens rows stays harmless.  Tokens past
+ * that a captured step of total_tokens rows stays harmless.  dummy_row must
+ * be a row that no request holds.  A request that goes on all the same after
+ * its page lay past num_free has the rest of that page on dummy_row as well (its
+ * tokens there are lost) and takes pages again behind it.  Tokens past
  * total_tokens (the lengths add up to more: a caller error) get no row.
  *   cached_lens, extend_lens: device int32 [batch].
  *   free_pages: device int32 [num_free], page numbers, taken in order; the

@@ -749,8 +749,9 @@ def minisgl_build_slots(cached_lens: torch.Tensor, extend_lens: torch.Tensor, pa
     tokens in the pool get extend_lens[r] more, in pages taken from free_pages
     in order.  Writes page_table [B, W] in place and returns the step's Slots
     (into `out` if given).  cached_lens[r] < 0 marks a padding request, whose
-    rows are dummy_row.  pages_used > len(free_pages) says that pages ran out
-    (the tokens without one are on dummy_row)."""
+    rows are dummy_row, a row that no request holds.  pages_used >
+    len(free_pages) says that pages ran out (the tokens without one are on
+    dummy_row, and so are the later ones of the same page)."""
     B, total = cached_lens.numel(), int(total_tokens)
     if total < 0:
         raise MinisglError("total_tokens must not be negative")

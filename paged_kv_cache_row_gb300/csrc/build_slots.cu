@@ -150,6 +150,8 @@ __global__ void __launch_bounds__(SLOT_THREADS) build_slots_kernel(SlotArgs a, i
         for (int u = 0; u < SLOT_U; ++u) got[u] = from[u] ? *from[u] : 0;
 #pragma unroll
         for (int u = 0; u < SLOT_U; ++u) {
+            // a last row on dummy_row had no page: the rows behind dummy_row are not this request's
+            if (from[u] && !fresh[u] && got[u] == a.dummy_row) row[u] = 0;
             row[u] += fresh[u] ? (int)((uint32_t)got[u] * (uint32_t)a.page_size) : got[u];
             if (to[u]) *to[u] = row[u];
             if (base + u < a.total_tokens) {

@@ -102,6 +102,22 @@ def test_slots_out_of_pages():
     check_slots([5, 0, 9], [40, 33, 20], 64, 8, cap_pages=0)
 
 
+@pytest.mark.parametrize("dummy", [0, 1, 3, 99])
+def test_slots_after_running_out_of_pages(dummy):
+    """A request that goes on after its page lay past the free pages: the rest
+    of that page stays on the dummy row (the first of a page, inside one, the
+    last of one whose next row is another request's, past the pool), and the
+    page behind it is a new one."""
+    D = dummy
+    table = torch.full((2, 16), -1, dtype=torch.int32, device=DEV)
+    steps = [([0, 0], [2, 6], [1], [4, 5] + [D] * 6, 3), ([2, 6], [1, 3], [2], [6, D, D, 8], 1),
+             ([3, 9], [1, 1], [5], [7, 9], 0), ([4, 10], [2, 1], [5], [20, 21, 10], 1)]
+    for cached, extend, free, loc, used in steps:
+        s = mk.minisgl_build_slots(i32(cached), i32(extend), table, i32(free), 4, D, sum(extend))
+        assert s.out_loc.tolist() == loc and s.pages_used.item() == used
+    assert table.tolist() == [[4, 5, 6, 7, 20, 21] + [-1] * 10, [D] * 8 + [8, 9, 10] + [-1] * 5]
+
+
 def test_slots_tail_width_and_short_total():
     check_slots([3, 0], [4, 5], 32, 4, total=50)             # captured for 50 tokens
     check_slots([30, 0, 40], [10, 5, 3], 32, 4)              # past the table's width
