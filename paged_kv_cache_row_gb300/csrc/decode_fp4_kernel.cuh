@@ -469,15 +469,9 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     if (lay.subs < 1) return cudaErrorInvalidConfiguration;
     lay.stages = std::min((optin - lay.off_ring) / (lay.subs * stage), MAX_STAGES);
     const size_t smem = (size_t)lay.off_ring + (size_t)lay.stages * lay.subs * stage;
-    // Where every stream can have a group of its own it may be left whole: no
-    // schedule to sum, no partials, no merge launch, which saves about the time
-    // of 5 tiles.  A group then has up to `wide` tiles one after the other
-    // instead of its share of all tiles.  8 heads, d 128, whole against split:
-    // 16 requests 8.5 / 8.7 us at 128 tokens, 13.5 / 9.6 at 256; 256 requests
-    // 37 / 43 at 512, 67.5 / 68.6 at 1024.
     const int64_t sms = device_sm_count(), streams = (int64_t)a.batch * lay.hblocks;
-    const int64_t groups = sms * lay.subs, wide = (a.pt_width + TILE - 1) / TILE;
-    lay.whole = streams <= groups && (wide - 5) * groups <= wide * streams && a.split_tokens == 0;
+    const int64_t wide = (a.pt_width + TILE - 1) / TILE;
+    lay.whole = fp4::leave_whole(streams, sms * lay.subs, wide) && a.split_tokens == 0;
     // never more ranges than tiles could exist
     const int64_t max_tiles = streams * wide;
     const int64_t grid = std::max<int64_t>(1, std::min(sms, lay.whole ? streams : max_tiles));

@@ -1,5 +1,6 @@
 """The 4-bit decode's plan (csrc/decode_fp4_plan.h), compiled for the host:
-which bytes of a token's scales its copies read."""
+which bytes of a token's scales its copies read, and which calls leave every
+stream to one group of warps."""
 import ctypes
 import os
 import subprocess
@@ -16,6 +17,7 @@ int block_heads_(int h) { return block_heads(h); }
 int heads_of_block_(int h, int heads, int hb) { return heads_of_block(h, heads, hb); }
 int scale_piece_(int heads, int sb) { return scale_piece(heads, sb); }
 int piece_bytes_(int row, int off, int piece) { return piece_bytes(row, off, piece); }
+int leave_whole_(int streams, int groups, int wide) { return leave_whole(streams, groups, wide); }
 }
 """
 
@@ -50,3 +52,17 @@ def test_scale_copies_read_each_byte_of_a_row_once_and_no_other(plan, d):
                 read += range(hb * heads * sb + off, hb * heads * sb + off + n)
         assert read == list(range(H * sb)), H
         assert plan.piece_bytes_(heads * sb, 1 << 30, piece) == 0  # lanes without a piece
+
+
+@pytest.mark.parametrize("groups", [132, 152, 304, 608, 2432])
+def test_streams_are_left_whole_in_narrow_tables_only(plan, groups):
+    """A group that has a stream for itself takes up to the table's width alone,
+    while every other may be done after one tile: only a few tiles may depend
+    on how the lengths happen to lie, however close the batch is to the number
+    of groups."""
+    for streams in sorted({1, groups // 3, groups // 2, groups - 3, groups - 1, groups, groups + 1, 2 * groups}):
+        for wide in list(range(40)) + [256, 1024, 1 << 25]:
+            whole = plan.leave_whole_(streams, groups, wide)
+            assert not whole or (streams <= groups and wide <= 8), (streams, wide)
+            if wide <= 5:
+                assert whole == (streams <= groups)

@@ -372,6 +372,18 @@ def test_decode_short_tables(Hq, Hkv, d):
         check_decode(pool, q, pt, lens)
 
 
+@pytest.mark.parametrize("B", [149, 152, 153, 302, 304, 305])
+@pytest.mark.parametrize("width", [160, 256, 288, 2048])
+def test_decode_batches_near_the_number_of_groups(B, width):
+    """One request as long as the table is wide, empty ones and short ones, at
+    batches around one and two groups of warps on each of 152 SMs."""
+    lens = [(0, 1, 30, 33, 64, 7)[r % 6] for r in range(B)]
+    lens[B // 2] = width
+    pool, q, pt = make_decode(16, 8, 128, lens, 2100, B + width)
+    assert pt.shape[1] == width
+    check_decode(pool, q, pt, lens)
+
+
 @pytest.mark.parametrize("H,d", [(8, 128), (2, 128), (4, 64), (16, 128), (3, 64)])
 def test_scale_rows_that_start_anywhere(H, d):
     """Scale rows only d/16-byte aligned (a slice of wider rows), elements in
