@@ -19,8 +19,9 @@ Entry points (same names as the C ABI):
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
-from typing import NamedTuple, Optional, Sequence, Tuple, Union
+from typing import List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -660,6 +661,21 @@ def _kv_rows(t: torch.Tensor, name: str, n: int, row: int, index: int, what: str
     return strides[0] if n > 1 else row
 
 
+def _exponents(e, layers: int, name: str) -> List[int]:
+    """One exponent per layer from one integer (of any kind) or one per layer."""
+    try:
+        try:
+            e = [operator.index(e)] * layers
+        except TypeError:
+            e = list(e)
+        out = [int(x) for x in e]
+        if len(out) == layers and all(o == x and -64 <= o <= 64 for o, x in zip(out, e)):
+            return out
+    except (TypeError, ValueError, OverflowError):
+        pass
+    raise MinisglError(f"{name} must be one int or one per layer, in [-64, 64]")
+
+
 class KVPoolFP4:
     """A paged KV pool in 4 bits (the format is in include/minisgl.h): `data`
     uint8 (2, L, R, H_kv, d/2), two e2m1 elements to a byte, and `scales`
@@ -690,12 +706,7 @@ class KVPoolFP4:
                 raise MinisglError("pool rows must be (H_kv, ..) contiguous")
         self.data, self.scales, self.page_size = data, scales, page_size
         self.num_layers, self.num_rows, self.num_kv_heads, self.head_dim = L, R, H, d
-        exps = []
-        for e, nm in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-            e = [int(e)] * L if isinstance(e, int) else [int(x) for x in e]
-            if len(e) != L or any(x < -64 or x > 64 for x in e):
-                raise MinisglError(f"{nm} must be one int or one per layer, in [-64, 64]")
-            exps.append(e)
+        exps = _exponents(k_exp, L, "k_exp"), _exponents(v_exp, L, "v_exp")
         self.k_exp, self.v_exp = exps
         at = {p: _PoolFP4Desc(
             k_data=data.data_ptr(), v_data=data.data_ptr() + data.stride(0),

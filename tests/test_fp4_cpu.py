@@ -212,3 +212,16 @@ def test_slots_start_no_kernel_early():
     loads, so they must not be resident while build_slots writes them."""
     code = _code("build_slots.cu")
     assert "pdl_wait()" in code and "pdl_launch_dependents" not in code
+
+
+@pytest.mark.parametrize("e", [3, np.int64(3), np.int8(3), torch.tensor(3), [3, 3], (3, 3), np.array([3, 3]),
+                               torch.tensor([3, 3]), [np.int32(3), torch.tensor(3)]], ids=repr)
+def test_exponents_of_any_integer_kind(e):
+    assert mk._exponents(e, 2, "k_exp") == [3, 3]
+
+
+@pytest.mark.parametrize("e", [None, 1.5, [0.5, 0], np.float32(1), "12", [1], [1, 2, 3], 65, [0, -65], [0, None],
+                               [0, float("nan")], [0, float("inf")], torch.tensor(0.5)], ids=repr)
+def test_exponents_refused(e):
+    with pytest.raises(mk.MinisglError, match="k_exp must be"):
+        mk._exponents(e, 2, "k_exp")

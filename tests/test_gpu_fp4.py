@@ -666,6 +666,16 @@ def test_binding_refusals():
         mk.minisgl_build_slots(sl, sl.clone(), table, sl, 4, 0, 2, out=s._replace(seq_lens=sl))
 
 
+def test_exponents_of_a_pool():
+    """numpy and torch integers as exponents, and what is none refused as any other argument."""
+    pool = mk.KVPoolFP4.zeros(2, 4, 1, 64, k_exp=np.int64(-2), v_exp=torch.tensor([1, -3]))
+    assert pool.k_exp == [-2, -2] and pool.v_exp == [1, -3]
+    k = kv_like((4, 1, 64), 1).to(DEV)
+    check_store(pool, 1, k, k, np.arange(4))
+    with pytest.raises(mk.MinisglError, match="v_exp must be"):
+        mk.KVPoolFP4.zeros(2, 4, 1, 64, v_exp=np.float32(1))
+
+
 class Engine:
     """One layer of a serving engine over the 4-bit pool, by the public calls:
     slots, store, and extend or decode attention."""
