@@ -602,8 +602,16 @@ FP4_BLOCK = 16  # channels that share a scale
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None) or \
-    (lambda shape, strides, dtype: torch.empty_strided(shape, strides, dtype=dtype, device="cuda"))
+_quick_new = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
+
+
+def _new(shape, strides, dtype):
+    """A new tensor on the current device.  The quick form goes past torch's
+    own function, which fills new memory where deterministic algorithms are
+    asked for."""
+    if _quick_new is None or torch.are_deterministic_algorithms_enabled():
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    return _quick_new(shape, strides, dtype)
 
 
 def _on(stream, index: int):

@@ -666,6 +666,22 @@ def test_binding_refusals():
         mk.minisgl_build_slots(sl, sl.clone(), table, sl, 4, 0, 2, out=s._replace(seq_lens=sl))
 
 
+def test_outputs_are_filled_where_torch_fills_new_memory():
+    """With deterministic algorithms torch fills new tensors with NaN; rows of
+    a load that no request fills show it."""
+    pool = random_pool(1, 8, 1, 64, 1)
+    args = i32([[2, 3, 4]]), i32([2]), i32([1, 3]), 5
+    k = [x.double() for x in mk.minisgl_load_kv_fp4(pool, 0, *args)][0][1:3]
+    torch.use_deterministic_algorithms(True)
+    try:
+        got = mk.minisgl_load_kv_fp4(pool, 0, *args)
+    finally:
+        torch.use_deterministic_algorithms(False)
+    for x in got:
+        assert x.shape == (5, 1, 64) and torch.isnan(x).all(dim=(1, 2)).tolist() == [True, False, False, True, True]
+    assert torch.equal(got[0][1:3].double(), k)
+
+
 def test_exponents_of_a_pool():
     """numpy and torch integers as exponents, and what is none refused as any other argument."""
     pool = mk.KVPoolFP4.zeros(2, 4, 1, 64, k_exp=np.int64(-2), v_exp=torch.tensor([1, -3]))
