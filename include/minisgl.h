@@ -134,7 +134,7 @@ int minisgl_store_kv(const minisgl_kv_pool *pool, int32_t layer, const void *k, 
 /*
  * Workspace size for minisgl_decode_attn, in bytes, for up to `max_splits`
  * partial results per (request, KV head) (2 <= max_splits <= 256; 16 is a
- * good default).  Layout of a workspace of this size, for the record (the
+ * good default, 32 and more for minisgl_decode_attn_fp4).  Layout of a workspace of this size, for the record (the
  * caller does not need to read it):
  *   int32 split_count[batch * num_kv_heads]            (at offset 0, padded to 256 B)
  *   float lse[batch * num_q_heads * max_splits]        natural-log LSE per partial
@@ -542,9 +542,14 @@ int minisgl_load_kv_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const in
  * of minisgl_decode_attn (q and out bf16, n == 0 gives out = 0) with K and V
  * the values of the pool's rows, and pt_width <= 2^30.  Products accumulate
  * in fp32; softmax weights are rounded to fp16 (11 bits) for the product with V.
+ * split_tokens: as there, rounded up to 32.
  * workspace: as for minisgl_decode_attn (minisgl_decode_workspace_bytes);
  * nothing in it needs to start at zero, and calls that may run at the same
- * time need different workspaces.
+ * time need different workspaces.  Its splits count for a request and up to 8
+ * KV heads together, where minisgl_decode_attn has as many for each head: with
+ * few long requests a larger workspace lets more of the GPU work (one request
+ * of 32768 tokens, 8 KV and 64 query heads, head_dim 128: 96 us with 16 splits,
+ * 53 with 32, 47 with 256).
  */
 int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, const void *q,
                             int32_t num_q_heads, const int32_t *page_table, int32_t batch,

@@ -693,7 +693,8 @@ class KVPoolFP4:
     multiplied with, one int or one per layer.  Caller-owned device memory; a
     new pool's bytes should be zero (KVPoolFP4.zeros makes one).  With one KV
     head use pages of 16 rows or more: a row's 64 and 8 bytes from anywhere take
-    twice as long to read as when their neighbours are used too."""
+    longer to read than when their neighbours are used too (200 requests of 1k
+    to 8k tokens, 8 query heads: 50 us instead of 36)."""
 
     def __init__(self, data: torch.Tensor, scales: torch.Tensor, page_size: int = 1,
                  k_exp: Union[int, Sequence[int]] = 0, v_exp: Union[int, Sequence[int]] = 0):
@@ -844,7 +845,8 @@ def minisgl_load_kv_fp4(pool: KVPoolFP4, layer: int, page_table: torch.Tensor, l
 
 def decode_workspace_fp4(batch: int, num_q_heads: int, pool: KVPoolFP4, max_splits: int = 32) -> torch.Tensor:
     """A new workspace for minisgl_decode_attn_fp4 on the pool's device.  Calls
-    that may run at the same time need different ones."""
+    that may run at the same time need different ones.  For one or two requests
+    of many tokens more splits let more of the GPU work (256 at most)."""
     return torch.empty(minisgl_decode_workspace_bytes(batch, num_q_heads, pool.num_kv_heads, pool.head_dim,
                                                       max_splits), dtype=torch.uint8, device=pool.data.device)
 

@@ -16,7 +16,10 @@
 // one piece.  A CTA (one per SM) has as many such groups of warps as fit 16
 // warps, each with a range of tiles of its own.  The tiles of all requests are
 // cut evenly over the groups of all CTAs: contiguous ranges whose lengths
-// differ by at most one.
+// differ by at most one (in narrow tables a group may take a request whole:
+// decode_fp4_plan.h).  The workspace's splits bound the ranges of a request and
+// block of heads, which one request of 32768 tokens (64 query heads) shows: 96 us
+// with 16, 53 with 32, 47 with 256.
 //
 // Loads: each group has a ring of three or more stages with a full and an
 // empty mbarrier each.  The group's warps fetch a tile together, each its
@@ -28,8 +31,8 @@
 // Rows past a request's end repeat its last row; their weights are zero.
 //
 // Measured (8 KV heads, d 128, warm): 256 requests of 1k to 8k tokens in
-// single-row pages 149 us, 5.4 TB/s of algorithmic bytes; 32 of 8k to 32k in
-// 64-row pages 137 us.  With the arithmetic left out 144 and 127, with the
+// single-row pages 148 us, 5.4 TB/s of algorithmic bytes; 32 of 8k to 32k in
+// 64-row pages 136 us.  With the arithmetic left out 144 and 127, with the
 // loads left out 137 and 129: the two nearly balance, so that every instruction
 // of a tile counts (634 to 588 a warp took 152 and 143.5 us to these), and about
 // 10 us are the start of the pipeline, the last ranges and the merge.
