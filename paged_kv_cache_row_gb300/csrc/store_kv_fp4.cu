@@ -144,8 +144,7 @@ template <bool WIDE>
 __global__ void __launch_bounds__(MAX_THREADS, LOAD_RESIDENT / MAX_THREADS)
     load_kv_fp4_kernel(LoadFp4Args a, int blocks16, int toks, int tile_toks) {
     __shared__ int s_row[2][LOAD_TOKENS];  // pool row of each token, or -1
-    pdl_wait();
-    pdl_launch_dependents();
+    pdl_wait();  // no early start for the next kernel: store_kv may read the rows with non-coherent loads
     const int64_t tiles = ((int64_t)a.total_tokens + tile_toks - 1) / tile_toks;
     const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
     int req = -1;  // lane's request

@@ -225,3 +225,11 @@ def test_exponents_of_any_integer_kind(e):
 def test_exponents_refused(e):
     with pytest.raises(mk.MinisglError, match="k_exp must be"):
         mk._exponents(e, 2, "k_exp")
+
+
+def test_load_starts_no_kernel_early():
+    """minisgl_store_kv may put the loaded rows into a bf16 pool, and reads new
+    rows with non-coherent loads."""
+    store, load = _code("store_kv_fp4.cu").split("load_kv_fp4_kernel(", 1)
+    assert "pdl_launch_dependents()" in store
+    assert "pdl_wait()" in load and "pdl_launch_dependents" not in load

@@ -611,6 +611,38 @@ def test_calls_on_a_named_stream():
     assert all(torch.equal(o, want) for o in outs)
 
 
+def test_loaded_rows_into_a_bf16_pool():
+    """Slots, load and minisgl_store_kv in a captured chain whose buffers are
+    used again by every round: each round's rows arrive, not the last one's."""
+    H, d, n, rounds = 8, 128, 2000, 6
+    pools = [random_pool(1, n + 1, H, d, 100 + i) for i in range(rounds)]
+    bf = [torch.zeros((2, 1, n + 1, H, d), dtype=torch.bfloat16, device=DEV) for _ in range(rounds)]
+    table, none, some, free = i32([range(n)]), i32([0]), i32([n]), i32(range(n))
+    own = torch.zeros((1, n), dtype=torch.int32, device=DEV)
+    k, v = (torch.zeros((n, H, d), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    out = mk.Slots.empty(1, n)
+
+    def chain():
+        for i in range(rounds):
+            s = mk.minisgl_build_slots(none, some, own, torch.roll(free, i * 7), 1, n, n, out=out)
+            mk.minisgl_load_kv_fp4(pools[i], 0, table, s.seq_lens, s.q_offsets, n, k, v)
+            mk.minisgl_store_kv(mk.KVPool(bf[i]), 0, k, v, s.out_loc)
+    chain()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        chain()
+    for t in bf:
+        t.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    for i in range(rounds):
+        rows = np.roll(np.arange(n), i * 7)
+        for got, want in zip(bf[i][:, 0, rows], pool_values(pools[i])):
+            assert np.array_equal(got.double().cpu().numpy(), want[:n])
+
+
 FIRST_USE = """
 import torch, paged_kv_cache_row_gb300 as mk
 i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
