@@ -134,8 +134,8 @@ int minisgl_store_kv(const minisgl_kv_pool *pool, int32_t layer, const void *k, 
 /*
  * Workspace size for minisgl_decode_attn, in bytes, for up to `max_splits`
  * partial results per (request, KV head) (2 <= max_splits <= 256; 16 is a
- * good default, 32 and more for minisgl_decode_attn_fp4).  Layout of a workspace of this size, for the record (the
- * caller does not need to read it):
+ * good default, 32 and more for minisgl_decode_attn_fp4).  Layout of a
+ * workspace of this size, for the record (the caller does not need to read it):
  *   int32 split_count[batch * num_kv_heads]            (at offset 0, padded to 256 B)
  *   float lse[batch * num_q_heads * max_splits]        natural-log LSE per partial
  *   float o[batch * num_q_heads * max_splits * head_dim] normalised partial outputs
