@@ -25,6 +25,7 @@
 #pragma once
 #include <cstdint>
 
+#include "decode_split.cuh"
 #include "fp4.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
@@ -32,8 +33,8 @@
 namespace minisgl {
 namespace fp4 {
 
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
+using split::LN2;
+using split::movmatrix_t;
 constexpr float REF_START = -3.402823466e38f;  // no finite score is below: the first tile sets the reference
 constexpr float REF_BELOW = 8.f;     // the reference starts this far below the maximum (base 2)
 constexpr float REF_ROOM = 15.f;     // and moves when a score passes it by more: 2^15 fits fp16
@@ -48,31 +49,6 @@ struct Head {
     static constexpr int OPT = D / 8;         // channels of a lane group in PV
 };
 
-__device__ __forceinline__ int clamp_len(int n, int w) { return min(max(n, 0), w); }
-
-__device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                              uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};\n"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The same with a zero accumulator.
-__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                                    uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%10,%10,%10,%10};\n"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-
-// Transpose an 8x8 b16 matrix held in the mma fragment layout.
-__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
-    return y;
-}
-
 __device__ __forceinline__ uint32_t lds_u8(uint32_t ad) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(ad));
@@ -83,18 +59,6 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t ad) {
     asm volatile("ld.shared.u16 %0, [%1];\n" : "=h"(v) : "r"(ad));
     return v;
 }
-template <int WORDS>
-__device__ __forceinline__ void lds_words(uint32_t ad, uint32_t (&w)[WORDS]) {
-    if constexpr (WORDS == 4)
-        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
-                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                     : "r"(ad));
-    else if constexpr (WORDS == 2)
-        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(ad));
-    else
-        asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(w[0]) : "r"(ad));
-}
-
 // A tile in shared memory: one record per token of 32, [K rows of all heads,
 // V rows, K scales, V scales], records `stride` bytes apart with
 // stride % 128 == 32 or 96.  Token x lies in slot slot(x).  The lanes' reads
@@ -128,41 +92,10 @@ struct Stream {
 
     // Loads the group's queries (q: G rows of D; null leaves zeros) and clears the sums.
     __device__ __forceinline__ void open(const __nv_bfloat16 *q, int G, float scale_log2, int lane) {
-        const int lg = lane >> 2, lt = lane & 3;
+        const int lt = lane & 3;
 #pragma unroll
         for (int n = 0; n < NG; ++n) {
-            const int h = n * 8 + lg;
-            uint32_t w[C::QPT / 2];  // this lane's channels of head h
-#pragma unroll
-            for (int i = 0; i < C::QPT / 2; ++i) w[i] = 0u;
-            if (h < G && q) {
-                const __nv_bfloat16 *src = q + h * D + lt * C::QPT;
-#pragma unroll
-                for (int i = 0; i < C::QPT / 8; ++i) {
-                    const uint4 v = reinterpret_cast<const uint4 *>(src)[i];
-                    w[4 * i] = v.x;
-                    w[4 * i + 1] = v.y;
-                    w[4 * i + 2] = v.z;
-                    w[4 * i + 3] = v.w;
-                }
-            }
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < C::QPT / 2; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-            m = max(m & 0xffffu, m >> 16);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            // largest |q| in [2^(b-127), 2^(b-126)): times 2^(141-b) it is below 2^15
-            const int b = max((int)(m >> 7), 20);
-            const float up = __int_as_float((268 - b) << 23);
-            const float down = __int_as_float((b - 14) << 23) * scale_log2;
-#pragma unroll
-            for (int ks = 0; ks < C::KS; ++ks)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t x = w[2 * ks + i];
-                    qb[n][ks][i] = f32_to_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
-                }
+            const float down = split::load_queries<D>(q, n * 8, G, scale_log2, lane, qb[n]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 sc[n][e] = __shfl_sync(0xffffffffu, down, (2 * lt + e) * 4);
@@ -371,189 +304,6 @@ struct Stream {
                     if (lg == 0) a.ws_lse[hh * a.max_splits + split] = (ref[n][e] + __log2f(sum)) * LN2;
                 }
             }
-    }
-};
-
-// ---- the cut of the work into ranges ---------------------------------------
-constexpr int TILE = 32;  // tokens of a tile
-
-// A tile: its request and head block, and the tokens from its first one to
-// the end of the request's context.
-struct Cursor {
-    int r, hb, left;
-};
-
-// Every CTA derives the same schedule from seq_lens: the tiles of all streams
-// (request, head block) in a row, cut into nseg ranges whose lengths differ
-// by at most one tile (32-bit arithmetic: all tiles together are below 2^31).  The prefix sums are kept for every CHUNK-th request
-// only, so that they leave room for the rings at the largest batch.
-constexpr int CHUNK = 4;
-__host__ __device__ constexpr int schedule_ints(int batch) { return (batch + CHUNK - 1) / CHUNK + 2; }
-
-struct Schedule {
-    const int32_t *prefix;  // shared: tiles before request CHUNK * k, then all tiles
-    const int32_t *seq_lens;
-    int batch, W, hblocks, chunks, total;
-    bool whole;             // range i is stream i
-    int nseg, each, more;   // ranges, tiles of each, how many have one more
-
-    // Called by all threads of the CTA (it synchronises them); s_prefix has
-    // room for schedule_ints(batch).  With whole there is nothing to sum.
-    __device__ __forceinline__ void init(int32_t *s_prefix, const DecodeArgs &a, int hblocks_, int ranges,
-                                         bool whole_) {
-        whole = whole_;
-        prefix = s_prefix;
-        seq_lens = a.seq_lens;
-        batch = a.batch;
-        W = a.pt_width;
-        hblocks = hblocks_;
-        chunks = (a.batch + CHUNK - 1) / CHUNK;
-        if (whole) {
-            nseg = a.batch * hblocks;
-            total = 1;
-            __syncthreads();
-            return;
-        }
-        // every thread sums the tiles of its chunks, then a scan over the CTA
-        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-        __shared__ int s_sum[32], s_max[32];
-        const int share = (chunks + blockDim.x - 1) / blockDim.x;
-        const int busy = (chunks + 32 * share - 1) / (32 * share);  // warps that have any
-        const int k0 = min(tid * share, chunks), k1 = min(k0 + share, chunks);
-        int mine = 0, mx = 0;
-        for (int k = k0; k < k1; ++k) {
-            int nt[CHUNK];
-            chunk_tiles(k, nt);
-#pragma unroll
-            for (int q = 0; q < CHUNK; ++q) {
-                mine += nt[q];
-                mx = max(mx, nt[q]);
-            }
-        }
-        mine *= hblocks;
-        int inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (chunks <= 32) {  // warp 0 has them all
-            if (warp == 0 && lane < chunks) s_prefix[lane] = inc - mine;
-            if (tid == 31) {
-                s_prefix[chunks] = inc;
-                s_prefix[chunks + 1] = mx;
-            }
-        } else {
-            if (lane == 31) {
-                s_sum[warp] = inc;
-                s_max[warp] = mx;
-            }
-            __syncthreads();
-            int at = inc - mine;  // tiles before this thread's chunks
-            for (int w = 0; w < min(warp, busy); ++w) at += s_sum[w];
-            for (int k = k0; k < k1; ++k) {
-                s_prefix[k] = at;
-                if (share == 1) break;
-                int nt[CHUNK];
-                chunk_tiles(k, nt);
-#pragma unroll
-                for (int q = 0; q < CHUNK; ++q) at += nt[q] * hblocks;
-            }
-            if (tid == 0) {
-                int all = 0, longest = 0;
-                for (int w = 0; w < busy; ++w) {
-                    all += s_sum[w];
-                    longest = max(longest, s_max[w]);
-                }
-                s_prefix[chunks] = all;
-                s_prefix[chunks + 1] = longest;
-            }
-        }
-        __syncthreads();
-        total = s_prefix[chunks];
-        // nseg ranges of L = total / nseg >= 1 tiles, the first `more` with one
-        // more.  A stream of nt tiles meets at most (nt - 2) / L + 2 of them, and
-        // L >= (nt - 1) / (max_splits - 1) keeps that within max_splits.
-        const int longest = s_prefix[chunks + 1];
-        nseg = ranges;
-        each = (uint32_t)total / (uint32_t)ranges;
-        if (a.split_tokens > 0 || each == 0 || (int64_t)each * (a.max_splits - 1) < longest) {
-            int want = a.split_tokens > 0 ? (int)(((int64_t)a.split_tokens + TILE - 1) / TILE) : 1;
-            want = max(want, (longest + a.max_splits - 2) / (a.max_splits - 1));
-            const int most = total / want;
-            nseg = max(1, a.split_tokens > 0 ? most : min(ranges, most));
-            each = total / nseg;
-        }
-        more = total - each * nseg;
-    }
-    __device__ __forceinline__ int begin(int seg) const { return seg * each + min(seg, more); }
-    // the range that holds tile t
-    __device__ __forceinline__ int range_of(int t) const {
-        const int longer = more * (each + 1);  // tiles of the longer ranges
-        return t < longer ? t / (each + 1) : more + (t - longer) / each;
-    }
-    __device__ __forceinline__ int len(int r) const { return clamp_len(seq_lens[r], W); }
-    __device__ __forceinline__ int tiles(int r) const { return (len(r) + TILE - 1) / TILE; }
-    // the same of a chunk's requests, all loads at once
-    __device__ __forceinline__ void chunk_tiles(int k, int (&nt)[CHUNK]) const {
-#pragma unroll
-        for (int q = 0; q < CHUNK; ++q) nt[q] = k * CHUNK + q < batch ? seq_lens[k * CHUNK + q] : 0;
-#pragma unroll
-        for (int q = 0; q < CHUNK; ++q) nt[q] = (clamp_len(nt[q], W) + TILE - 1) / TILE;
-    }
-    // tiles before head block hb of request r
-    __device__ __forceinline__ int before(int r, int hb) const {
-        int nt[CHUNK], t = prefix[r / CHUNK];
-        chunk_tiles(r / CHUNK, nt);
-#pragma unroll
-        for (int q = 0; q < CHUNK; ++q) t += nt[q] * (q < r % CHUNK ? hblocks : q == r % CHUNK ? hb : 0);
-        return t;
-    }
-    __device__ __forceinline__ void locate(Cursor &c, int t) const {
-        int lo = 0, hi = chunks;  // largest chunk with prefix <= t: it holds tile t
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (prefix[mid] <= t) lo = mid; else hi = mid;
-        }
-        int off = t - prefix[lo], nt[CHUNK], q = 0;
-        chunk_tiles(lo, nt);
-        int n = nt[0];
-#pragma unroll
-        for (int i = 1; i < CHUNK; ++i)
-            if (q == i - 1 && off >= n * hblocks) {
-                off -= n * hblocks;
-                n = nt[i];
-                q = i;
-            }
-        c.r = lo * CHUNK + q;
-        c.hb = hblocks == 1 ? 0 : off / n;
-        c.left = len(c.r) - (off - c.hb * n) * TILE;
-    }
-    // Tiles of range seg.
-    __device__ __forceinline__ int range_tiles(int seg) const {
-        return whole ? tiles(seg / hblocks) : begin(seg + 1) - begin(seg);
-    }
-    // The same, and its first tile (with no tiles: the stream).
-    __device__ __forceinline__ int range(int seg, Cursor &c) const {
-        if (whole) {
-            c.r = hblocks == 1 ? seg : seg / hblocks;
-            c.hb = seg - c.r * hblocks;
-            c.left = len(c.r);
-            return (c.left + TILE - 1) / TILE;
-        }
-        const int t = begin(seg);
-        locate(c, t);
-        return begin(seg + 1) - t;
-    }
-    // To the first tile of the next stream (there is one).
-    __device__ __forceinline__ void next_stream(Cursor &c) const {
-        if (++c.hb == hblocks) {
-            c.hb = 0;
-            do { ++c.r; } while (len(c.r) == 0);
-        }
-        c.left = len(c.r);
     }
 };
 

@@ -3,7 +3,7 @@
 //     out[r,h] = sum_j softmax_j(sm_scale <q[r,h], K_j>) V_j,   j < seq_len[r],
 // K_j and V_j the values c * s * 2^exp of row page_table[r, j] (the pool's
 // format is in the public header).  Split partials are merged by
-// decode_fp4_merge_kernel.
+// split::decode_merge_kernel.
 //
 // What bounds it: the K/V bytes, 2 * (d/2 + d/16) a token and KV head, 144 at
 // d 128.  At the card's copy rate that is 43 elements a cycle and SM, so the
@@ -48,12 +48,10 @@
 #pragma once
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 #include <type_traits>
 
 #include "decode_fp4.cuh"
 #include "decode_fp4_plan.h"
-#include "tcgen05.cuh"
 
 namespace minisgl {
 
@@ -61,17 +59,23 @@ namespace {
 
 __device__ unsigned int fp4_timeouts = 0;  // one per translation unit
 
-using fp4::Cursor;
 using fp4::Head;
-using fp4::Schedule;
-using fp4::TILE;
+using split::align_up;
+using split::cp_async_arrive;
+using split::Cursor;
+using split::guarded_wait;
+using split::ld_s32;
+using split::log2_up;
+using split::raise_limit;
+using split::row_at;
+using split::Schedule;
+using split::TILE;
 
 // Warps per CTA (one CTA per SM): 16 at up to 128 registers each; the 16-head
 // form at d 128 needs more.
 template <int D, int NG>
 constexpr int MAX_WARPS = D == 128 && NG == 2 ? 8 : 16;
 constexpr int MAX_STAGES = 8;
-constexpr long long WAIT_LIMIT = 1000000000LL;  // SM cycles (about 0.5 s)
 
 // How a CTA's warps and shared memory are laid out (set by the host).
 struct Layout {
@@ -82,8 +86,6 @@ struct Layout {
     int off_bars, off_ring;
 };
 
-constexpr int log2_up(int x) { return x <= 1 ? 0 : 1 + log2_up((x + 1) / 2); }
-
 // Bytes between the token records of `heads` heads.
 template <int D>
 __host__ __device__ constexpr int record_stride(int heads) {
@@ -92,40 +94,10 @@ __host__ __device__ constexpr int record_stride(int heads) {
     return s;
 }
 
-// Bounded wait: once one wait has run out, the CTA stops waiting altogether,
-// so every warp reaches the end (the output is then garbage and counted).
-__device__ __forceinline__ void guarded_wait(uint32_t b, uint32_t parity, volatile int *abort_flag) {
-    if (mbar_try_wait(b, parity)) return;
-    if (*abort_flag) return;
-    if (!mbar_wait(b, parity, WAIT_LIMIT)) {
-        *abort_flag = 1;
-        atomicAdd(&fp4_timeouts, 1u);
-    }
-}
-
 template <int N>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
-// base + row * stride, one multiply-add for each of K and V instead of a product and two sums
-__device__ __forceinline__ const uint8_t *row_at(const uint8_t *base, uint32_t row, uint32_t stride) {
-    const uint8_t *p;
-    asm("mad.wide.u32 %0, %1, %2, %3;\n" : "=l"(p) : "r"(row), "r"(stride), "l"(base));
-    return p;
-}
-// A coherent load (the step's slots may still be written when this kernel
-// starts), and one that stays behind the copies it follows in the source: left
-// to the compiler's order it took 148 us where 136 are taken.
-__device__ __forceinline__ int ld_s32(const int32_t *p) {
-    int v;
-    asm volatile("ld.global.s32 %0, [%1];\n" : "=r"(v) : "l"(p));
-    return v;
-}
-// One arrival on `bar` when this thread's cp.async copies so far have landed.
-__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
-}
-
 }  // namespace
 
 // HEADS: KV heads of a head block, one warp each (the record stride and the
@@ -221,7 +193,7 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
             sbytes = fp4::piece_bytes(nh * C::SB, soff, WIDE);
             in_hb = hb;
         }
-        guarded_wait(bar + 8u, in_parity, &s_abort);
+        guarded_wait(bar + 8u, in_parity, &s_abort, &fp4_timeouts);
 #pragma unroll
         for (int i0 = 0; i0 < MOST; i0 += TOKS) {
             const int i = i0 + sub_tok;
@@ -318,7 +290,7 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
             const int n = min(use, (c.left + TILE - 1) / TILE), end = c.left - n * TILE;
             use -= n;
             for (; c.left > end; c.left -= TILE) {
-                guarded_wait(bars + at * 16u, parity, &s_abort);
+                guarded_wait(bars + at * 16u, parity, &s_abort, &fp4_timeouts);
                 const uint32_t st = at * stage_bytes;
                 uint32_t pb[2][NG][2];
                 if (live) {
@@ -351,104 +323,6 @@ __global__ void __launch_bounds__(MAX_WARPS<D, NG> * 32, 1)
 
 namespace {
 
-// Joins the partials of the streams that were cut, one warp per (request, query
-// head) row: out = sum_k w_k O_k / sum_k w_k, w_k = e^(LSE_k - max LSE).  Rows
-// that are whole hold their output already; empty requests get zeros.
-//
-// What bounds it are rounds of dependent loads, about 1 us each behind the
-// launch, and how many rows are under way.  There are two rounds: the length
-// and the count, then the LSEs and MOST partials.  MOST 16 takes 96 registers
-// and so 2432 rows at once, MOST 4 takes 40 and three times as many: 16 takes
-// 0.9 us less for 1024 rows in 2-3 partials, 1.5 less for 2048 rows in about 10,
-// 2.7 more for 8192 rows in 2-3.
-template <int D, int MOST>
-__global__ void __launch_bounds__(128, MOST > 8 ? 4 : 12) decode_fp4_merge_kernel(const DecodeArgs a) {
-    constexpr int CPL = D / 32;  // channels per lane
-    const int Hkv = a.num_kv_heads, Hq = a.num_q_heads;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_launch_dependents();
-    if (row >= a.batch * Hq) return;
-    const int r = row / Hq, g = (row - r * Hq) / (Hq / Hkv);
-    const int len = a.seq_lens[r], cnt = a.split_count[(int64_t)r * Hkv + g];
-    const int n = fp4::clamp_len(len, a.pt_width) == 0 ? 0 : min(cnt, a.max_splits);  // no count without context
-    if (n == 1) return;
-    const int64_t base = (int64_t)row * a.max_splits;
-    const float l0 = lane < n ? a.ws_lse[base + lane] : -INFINITY;
-    float M = l0;
-    for (int s = 32 + lane; s < n; s += 32) M = fmaxf(M, a.ws_lse[base + s]);
-    const float *src = a.ws_o + base * D + lane * CPL;  // of partial k at src + k * D
-    float acc[CPL], tot = n == 0 ? 1.f : 0.f;
-#pragma unroll
-    for (int c = 0; c < CPL; ++c) acc[c] = 0.f;
-    for (int k0 = 0; k0 < n; k0 += MOST) {
-        float x[MOST][CPL];
-#pragma unroll
-        for (int k = 0; k < MOST; ++k)
-            if (k0 + k < n) {
-                if constexpr (CPL == 4) {
-                    const float4 v = *reinterpret_cast<const float4 *>(src + (k0 + k) * D);
-                    x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
-                } else {
-                    const float2 v = *reinterpret_cast<const float2 *>(src + (k0 + k) * D);
-                    x[k][0] = v.x, x[k][1] = v.y;
-                }
-            }
-        if (k0 == 0) {  // while the first rows come
-#pragma unroll
-            for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        }
-        // the weights, in the first MOST lanes
-        const float w = lane < MOST && k0 + lane < n ? __expf((k0 ? a.ws_lse[base + k0 + lane] : l0) - M) : 0.f;
-#pragma unroll
-        for (int k = 0; k < MOST; ++k)
-            if (k0 + k < n) {
-                const float wk = __shfl_sync(0xffffffffu, w, k);
-                tot += wk;
-#pragma unroll
-                for (int c = 0; c < CPL; ++c) acc[c] += wk * x[k][c];
-            }
-    }
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)row * D + lane * CPL;
-    const float inv = 1.f / tot;
-#pragma unroll
-    for (int c = 0; c < CPL; c += 2)
-        *reinterpret_cast<uint32_t *>(out + c) = pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
-}
-
-// The kernel's shared-memory limit raised to the device's, once per device.
-template <typename K>
-cudaError_t raise_limit(K kernel, int &optin) {
-    struct Entry { const void *fn; int dev, optin; };
-    static std::mutex mu;
-    static Entry cache[64];
-    static int used = 0;
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lk(mu);
-    for (int i = 0; i < used; ++i)
-        if (cache[i].fn == (const void *)kernel && cache[i].dev == dev) {
-            optin = cache[i].optin;
-            return cudaSuccess;
-        }
-    cudaFuncAttributes fa;
-    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
-    if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
-    if (e == cudaSuccess) {
-        optin -= (int)fa.sharedSizeBytes;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, optin);
-    }
-    if (e != cudaSuccess) {
-        cudaGetLastError();  // do not leave the failure for the next caller to find
-        return e;
-    }
-    if (used < 64) cache[used++] = {(const void *)kernel, dev, optin};
-    return cudaSuccess;
-}
-
-int align_up(int x, int a) { return (x + a - 1) / a * a; }
-
 template <int D, int NG, int HEADS>
 cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     const DecodeArgs &a = args.d;
@@ -466,7 +340,7 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     // as many groups as leave three stages to each
     constexpr int stage = TILE * record_stride<D>(HEADS);
     lay.subs = MAX_WARPS<D, NG> / HEADS;
-    lay.off_bars = align_up(fp4::schedule_ints(a.batch) * 4, 16);
+    lay.off_bars = align_up(split::schedule_ints(a.batch) * 4, 16);
     lay.off_ring = align_up(lay.off_bars + MAX_STAGES * lay.subs * 16, 128);
     lay.subs = std::min(lay.subs, (optin - lay.off_ring) / (3 * stage));
     if (lay.subs < 1) return cudaErrorInvalidConfiguration;
@@ -479,10 +353,10 @@ cudaError_t launch_cfg(const DecodeFp4Args &args, cudaStream_t s) {
     const int64_t max_tiles = streams * wide;
     const int64_t grid = std::max<int64_t>(1, std::min(sms, lay.whole ? streams : max_tiles));
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(HEADS * lay.subs * 32), smem, s, args,
-                   a.sm_scale * fp4::LOG2E * ldexpf(1.f, p.k_exp), ldexpf(1.f, p.v_exp), lay);
+                   a.sm_scale * split::LOG2E * ldexpf(1.f, p.k_exp), ldexpf(1.f, p.v_exp), lay);
     if (e != cudaSuccess || lay.whole) return e;
     const int64_t rows = (int64_t)a.batch * a.num_q_heads;  // up to 4 CTAs of 4 an SM: the wide form
-    return launch_pdl(rows <= 16 * sms ? decode_fp4_merge_kernel<D, 16> : decode_fp4_merge_kernel<D, 4>,
+    return launch_pdl(rows <= 16 * sms ? split::decode_merge_kernel<D, 16> : split::decode_merge_kernel<D, 4>,
                       dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a);
 }
 
