@@ -19,6 +19,16 @@
  *   minisgl_load_kv_fp4      read cached rows back as packed bf16 rows (for extend attention)
  *   minisgl_decode_attn_fp4  decode attention over the 4-bit pool
  *
+ * The same over a pool that keeps them in 8 bits with a scale per block of
+ * tokens and head (minisgl_kv_pool_fp8), and the rotary tables of long contexts:
+ *
+ *   minisgl_rope_table       cos/sin rows for positions (frequencies: minisgl_rope_frequencies)
+ *   minisgl_rope_store_kv_fp8  rotate q and k (half-split or interleaved pairs, part of the
+ *                            head), quantise k and v into the 8-bit pool
+ *   minisgl_store_kv_fp8     the same for rows that are rotated already
+ *   minisgl_load_kv_fp8      read cached rows back as packed bf16 rows (for extend attention)
+ *   minisgl_decode_attn_fp8  decode attention over the 8-bit pool
+ *
  * Sources of the definitions (page title, section):
  *   [deep-dive]  "mini-sglang 架构深度解读" (mini-sglang architecture deep dive,
  *                tinymind.me): section 6.2 MHAKVCache layout, section 3.6
@@ -557,6 +567,157 @@ int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, cons
                             float sm_scale, void *out, void *workspace, size_t workspace_bytes,
                             int32_t split_tokens, void *stream);
 
+/*
+ * The rotary frequencies of a model, and the rows of the [cos | sin] table that
+ * minisgl_rope_store_kv and minisgl_rope_store_kv_fp8 read [deep-dive 7.3 RoPE:
+ * a float32 table per position].  With n = rotary_dim, f = factor and
+ * theta_j = base^(-2j/n), j < n/2, the frequency of pair j is, by kind,
+ *   PLAIN   theta_j
+ *   LINEAR  theta_j / f                      (positions interpolated)
+ *   NTK     theta_j with base * f^(n/(n-2)) for base: the slowest one is theta / f
+ *   BANDS   s theta_j / f + (1 - s) theta_j, with 1 - s = (t - slow_turns) /
+ *           (fast_turns - slow_turns) clamped to [0, 1] and t the turns that
+ *           theta_j makes in original_positions
+ *   YARN    the same with s = (j - lo) / (hi - lo) clamped to [0, 1], where
+ *           lo = floor(x(fast_turns)) >= 0, hi = ceil(x(slow_turns)) <= n - 1 and
+ *           x(t) = n ln(original_positions / (2 pi t)) / (2 ln base); hi = lo +
+ *           0.001 if it is not above lo.
+ * minisgl_rope_frequencies (on the host; it touches no GPU) writes them as
+ * turns[j] = frequency / (2 pi) * 2^64, rounded, and the factor of cos and sin:
+ * attention_factor, or if that is 0 then 0.1 ln f + 1 for YARN and 1 otherwise.
+ * rotary_dim: a multiple of 16, 16 .. 256.  factor >= 1 is not read for PLAIN;
+ * original_positions, slow_turns and fast_turns (0 < slow < fast; usual are 1
+ * and 4 for BANDS, 1 and 32 for YARN) are read for BANDS and YARN only.
+ */
+enum { MINISGL_ROPE_PLAIN = 0, MINISGL_ROPE_LINEAR = 1, MINISGL_ROPE_NTK = 2, MINISGL_ROPE_BANDS = 3,
+       MINISGL_ROPE_YARN = 4 };
+
+typedef struct {
+    int32_t kind;                /* MINISGL_ROPE_* */
+    int32_t rotary_dim;
+    double base;                 /* above 1 */
+    double factor;
+    double original_positions;
+    double slow_turns, fast_turns;
+    double attention_factor;     /* 0: by kind */
+} minisgl_rope;
+
+int minisgl_rope_frequencies(const minisgl_rope *rope, uint64_t *turns, float *attention);
+
+/*
+ * Rows of the table for positions [n]: with a_j = positions[i] * turns[j] / 2^64
+ * turns, exact modulo one turn,
+ *     out[i*rotary_dim + j] = attention * cos(a_j),  out[i*rotary_dim + rotary_dim/2 + j] = attention * sin(a_j).
+ * cos and sin are within 2^-22 of the exact ones (times attention); the rounding
+ * of turns adds at most |position| * 2^-53.  Positions may be any int32.  With
+ * positions 0, 1, 2, .. out is the table of the rotary calls; with a step's
+ * positions it has a row for each token, whose position in those calls is then
+ * its number.
+ *   turns: HOST, rotary_dim/2 values of minisgl_rope_frequencies (copied
+ *     before the call returns).  positions: device int32 [n].
+ *   out: device float32 [n, rotary_dim], 16-byte aligned.
+ */
+int minisgl_rope_table(const uint64_t *turns, float attention, int32_t rotary_dim, const int32_t *positions, int32_t n,
+                       float *out, void *stream);
+
+/*
+ * The KV pool in 8 bits.  block_tokens = B consecutive rows (rows bB .. bB+B-1)
+ * are a block of tokens.  A block has for each head, and for K and V apart, one
+ * power of two (a byte x, for 2^(x - 127)), and a channel of a row is an e4m3
+ * element c (a byte) and stands for c * 2^(x - 127):
+ *   channel c of (l, row, h) is byte  k_data + l*data_layer_stride + row*data_row_stride + h*head_dim + c
+ *   and its block's scale is byte    k_scale + l*scale_layer_stride + (row / B)*scale_block_stride + h
+ * All strides are in BYTES.  Half the memory of a bf16 pool.  The rows of a
+ * block belong to one request (B divides page_size), B is 1, 16, 32 or 64, and
+ * there are ceil(num_rows / B) blocks.  data bases and strides are multiples of
+ * 16 bytes, scale bases and strides multiples of 4, and a block's scales have
+ * num_kv_heads bytes and room up to the next multiple of 4 (whose bytes are
+ * read and never used); strides of rows and blocks are below 2^31 bytes.
+ * Scales are 1 .. 254 (a store writes 7 .. 246); 0 and 255 give unspecified values.
+ */
+enum { MINISGL_FP8 = 3 };
+
+typedef struct {
+    void *k_data, *v_data;       /* device: e4m3 elements of layer 0, row 0 */
+    void *k_scale, *v_scale;     /* device: scales of layer 0, block 0 */
+    int64_t data_layer_stride, data_row_stride;      /* bytes; row >= num_kv_heads*head_dim */
+    int64_t scale_layer_stride, scale_block_stride;  /* bytes; block >= num_kv_heads rounded up to 4 */
+    int32_t num_layers;
+    int32_t num_rows;
+    int32_t num_kv_heads;        /* 1 .. 4096 */
+    int32_t head_dim;            /* 64 or 128 */
+    int32_t page_size;           /* a multiple of block_tokens */
+    int32_t block_tokens;        /* 1, 16, 32 or 64 */
+    int32_t dtype;               /* MINISGL_FP8 */
+} minisgl_kv_pool_fp8;
+
+/*
+ * store_kv into the 8-bit pool [learn, paged KV pool: store_kv passage].  The
+ * new rows of a block must follow one another in out_loc and in the pool, as
+ * minisgl_build_slots lays them out (a run: row, row + 1, ..; at most one in a
+ * block and call).  For a run in block b and every KV head h of k (and of v):
+ *     need = the smallest e, -120 <= e <= 119, with |x| <= 448 * 2^e for all its finite x,
+ *     e = need if the run begins at the block's first row, else max(need, the block's e so far),
+ *     element = e4m3(x * 2^-e), rounded to nearest, ties to even, saturating at 448,
+ * and if e grew, the block's rows before the run become e4m3(c * 2^(e_before - e))
+ * (exact but for elements that turn subnormal).  Rows of the block behind the
+ * run hold nothing afterwards.  A NaN stays one and an infinity becomes one
+ * (e4m3 has no infinity); neither counts for e.  Arguments as minisgl_store_kv
+ * (k, v bf16, strides in elements).  Tokens that share a row (CUDA-graph padding
+ * on dummy_row) race and leave it, and the rows of its block, unspecified: no
+ * request may hold a row of the dummy row's block.
+ */
+int minisgl_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const void *k, const void *v,
+                         int64_t k_tok_stride, int64_t v_tok_stride, const int32_t *out_loc, int32_t n_tokens,
+                         void *stream);
+
+/*
+ * The same with rotary position embedding on the way [deep-dive 7.3 RoPE].  The
+ * first rotary_dim channels of every head of q and k are rotated in pairs,
+ * (j, j + rotary_dim/2), or (2j, 2j + 1) if interleaved, j < rotary_dim/2, by
+ * the row p = positions[i] of cos_sin_cache, [cos | sin]:
+ *     y = x cos_j(p) - x' sin_j(p),   y' = x' cos_j(p) + x sin_j(p)   for the pair (x, x');
+ * the other channels stay.  q is rounded to bf16 and written to q_out, which
+ * may be q itself (same strides; else they must not overlap).  k is quantised
+ * from its fp32 rotation and left as it was.
+ *   q, q_out: device bf16, [num_q_heads, head_dim] per token (token strides in
+ *     elements, multiples of 8); num_q_heads may be 0, q then NULL.
+ *   positions, out_loc: device int32 [n_tokens].
+ *   cos_sin_cache: device float32 [max_positions, rotary_dim], 16-byte aligned.
+ *   rotary_dim: a multiple of 16, 16 .. head_dim.
+ * Positions outside [0, max_positions) and rows outside [0, num_rows) are a
+ * caller error: they are clamped into range (results unspecified).
+ */
+int minisgl_rope_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                              int64_t q_tok_stride, void *q_out, int64_t q_out_tok_stride, const void *k,
+                              const void *v, int64_t k_tok_stride, int64_t v_tok_stride, const int32_t *positions,
+                              const float *cos_sin_cache, int32_t max_positions, int32_t rotary_dim,
+                              int32_t interleaved, const int32_t *out_loc, int32_t n_tokens, void *stream);
+
+/*
+ * Rows of the 8-bit pool as packed bf16 rows: as minisgl_load_kv_fp4, with the
+ * values of the 8-bit pool's rows, which are exact in bf16 (for scales that a
+ * store gives).  Rows that no request fills are left as they were.
+ */
+int minisgl_load_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const int32_t *page_table, int32_t batch,
+                        int64_t pt_row_stride, int32_t pt_width, const int32_t *lens, const int32_t *offsets,
+                        int32_t total_tokens, void *k_out, void *v_out, int64_t k_tok_stride, int64_t v_tok_stride,
+                        void *stream);
+
+/*
+ * Decode attention over the 8-bit pool: the definition, arguments and limits of
+ * minisgl_decode_attn (q and out bf16, n == 0 gives out = 0) with K and V the
+ * values of the pool's rows (in any order: page_table holds raw rows), and
+ * pt_width <= 2^30.  Products accumulate in fp32; softmax weights are rounded to
+ * fp16 (11 bits) for the product with V.  split_tokens and workspace: as for
+ * minisgl_decode_attn_fp4 (splits count for a request and up to 8 KV heads
+ * together: with few long requests a larger workspace lets more of the GPU work).
+ */
+int minisgl_decode_attn_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                            const int32_t *page_table, int32_t batch, int64_t pt_row_stride, int32_t pt_width,
+                            const int32_t *seq_lens, float sm_scale, void *out, void *workspace,
+                            size_t workspace_bytes, int32_t split_tokens, void *stream);
+
 /* Message of the last error on the calling thread ("" if none). */
 const char *minisgl_last_error(void);
 
@@ -577,9 +738,9 @@ int32_t minisgl_device_sm_count(void);
 int minisgl_debug_set_pdl(int enabled);
 
 /* Debugging aid: how many bounded waits inside the tensor-core kernels and
- * the 4-bit decode kernel ran out of time since the library was loaded on
- * the current device.  A non-zero count means some minisgl_extend_attn or
- * minisgl_decode_attn_fp4 output is garbage.  This call
+ * the 4-bit and 8-bit decode kernels ran out of time since the library was
+ * loaded on the current device.  A non-zero count means some minisgl_extend_attn,
+ * minisgl_decode_attn_fp4 or minisgl_decode_attn_fp8 output is garbage.  This call
  * synchronises with the device (it reads a device counter), so it is not
  * for the hot path. */
 int minisgl_debug_timeout_count(uint32_t *count);

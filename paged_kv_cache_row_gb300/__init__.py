@@ -15,6 +15,11 @@ Entry points (same names as the C ABI):
     minisgl_store_kv_fp4(pool, layer, k, v, out_loc)                    (pool: a KVPoolFP4)
     minisgl_load_kv_fp4(pool, layer, page_table, lens, offsets, total_tokens)
     minisgl_decode_attn_fp4(pool, layer, q, page_table, seq_lens, sm_scale, ...)
+    minisgl_rope_table(rope, positions)                                 (rope: a Rope)
+    minisgl_rope_store_kv_fp8(pool, layer, q, k, v, positions, cos_sin_cache, out_loc, ...)
+    minisgl_store_kv_fp8(pool, layer, k, v, out_loc)                    (pool: a KVPoolFP8)
+    minisgl_load_kv_fp8(pool, layer, page_table, lens, offsets, total_tokens)
+    minisgl_decode_attn_fp8(pool, layer, q, page_table, seq_lens, sm_scale, ...)
 """
 from __future__ import annotations
 
@@ -37,6 +42,8 @@ __all__ = [
     "minisgl_cascade_extend_workspace_bytes", "minisgl_check_shared_prefix",
     "KVPoolFP4", "Slots", "minisgl_build_slots", "minisgl_store_kv_fp4", "minisgl_load_kv_fp4",
     "minisgl_decode_attn_fp4", "decode_workspace_fp4", "kv_pool_fp4_bytes",
+    "KVPoolFP8", "Rope", "minisgl_rope_table", "minisgl_rope_store_kv_fp8", "minisgl_store_kv_fp8",
+    "minisgl_load_kv_fp8", "minisgl_decode_attn_fp8", "decode_workspace_fp8", "kv_pool_fp8_bytes",
 ]
 
 EXPORTED_SYMBOLS = [
@@ -47,10 +54,13 @@ EXPORTED_SYMBOLS = [
     "minisgl_check_indices", "minisgl_debug_set_pdl", "minisgl_cascade_extend_attn",
     "minisgl_cascade_extend_workspace_bytes", "minisgl_check_shared_prefix",
     "minisgl_build_slots", "minisgl_store_kv_fp4", "minisgl_load_kv_fp4", "minisgl_decode_attn_fp4",
+    "minisgl_rope_frequencies", "minisgl_rope_table", "minisgl_store_kv_fp8", "minisgl_rope_store_kv_fp8",
+    "minisgl_load_kv_fp8", "minisgl_decode_attn_fp8",
 ]
 
 MINISGL_BF16 = 1
 MINISGL_FP4 = 2
+MINISGL_FP8 = 3
 
 
 class MinisglError(RuntimeError):
@@ -77,6 +87,28 @@ class _PoolFP4Desc(ctypes.Structure):
         ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
         ("page_size", ctypes.c_int32), ("dtype", ctypes.c_int32),
         ("k_exp", ctypes.c_int32), ("v_exp", ctypes.c_int32),
+    ]
+
+
+class _PoolFP8Desc(ctypes.Structure):
+    _fields_ = [
+        ("k_data", ctypes.c_void_p), ("v_data", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("data_layer_stride", ctypes.c_int64), ("data_row_stride", ctypes.c_int64),
+        ("scale_layer_stride", ctypes.c_int64), ("scale_block_stride", ctypes.c_int64),
+        ("num_layers", ctypes.c_int32), ("num_rows", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("block_tokens", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class _RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("kind", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("base", ctypes.c_double), ("factor", ctypes.c_double),
+        ("original_positions", ctypes.c_double), ("slow_turns", ctypes.c_double),
+        ("fast_turns", ctypes.c_double), ("attention_factor", ctypes.c_double),
     ]
 
 
@@ -144,6 +176,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.minisgl_decode_attn_fp4.argtypes = [P4, i32, vp, i32, vp, i32, i64, i32, vp, f32, vp, vp, sz, i32,
                                             vp]
     lib.minisgl_decode_attn_fp4.restype = ctypes.c_int
+    P8 = ctypes.POINTER(_PoolFP8Desc)
+    lib.minisgl_rope_frequencies.argtypes = [ctypes.POINTER(_RopeDesc), vp, ctypes.POINTER(f32)]
+    lib.minisgl_rope_frequencies.restype = ctypes.c_int
+    lib.minisgl_rope_table.argtypes = [vp, f32, i32, vp, i32, vp, vp]
+    lib.minisgl_rope_table.restype = ctypes.c_int
+    lib.minisgl_store_kv_fp8.argtypes = [P8, i32, vp, vp, i64, i64, vp, i32, vp]
+    lib.minisgl_store_kv_fp8.restype = ctypes.c_int
+    lib.minisgl_rope_store_kv_fp8.argtypes = [P8, i32, vp, i32, i64, vp, i64, vp, vp, i64, i64, vp, vp, i32, i32,
+                                              i32, vp, i32, vp]
+    lib.minisgl_rope_store_kv_fp8.restype = ctypes.c_int
+    lib.minisgl_load_kv_fp8.argtypes = [P8, i32, vp, i32, i64, i32, vp, vp, i32, vp, vp, i64, i64, vp]
+    lib.minisgl_load_kv_fp8.restype = ctypes.c_int
+    lib.minisgl_decode_attn_fp8.argtypes = [P8, i32, vp, i32, vp, i32, i64, i32, vp, f32, vp, vp, sz, i32,
+                                            vp]
+    lib.minisgl_decode_attn_fp8.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -882,4 +929,273 @@ def minisgl_decode_attn_fp4(pool: KVPoolFP4, layer: int, q: torch.Tensor, page_t
         pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B, stride, width, seq_lens.data_ptr(),
         float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, split_tokens,
         _raw_stream(dev)), "decode_attn_fp4")
+    return out
+
+
+# --------------------------------------------------------------------------- #
+# rotary tables
+# --------------------------------------------------------------------------- #
+_ROPE_KINDS = {"plain": 0, "linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+class Rope:
+    """The rotary frequencies of a model (their definition is in
+    include/minisgl.h): rotary_dim channels, base, and how they are scaled for
+    contexts `factor` times longer than original_positions: "plain" (not at
+    all), "linear", "ntk", "bands" or "yarn".  slow_turns and fast_turns are 1
+    and 4 for "bands" and 1 and 32 for "yarn" unless given; attention_factor,
+    which cos and sin are multiplied with, is 0.1 ln(factor) + 1 for "yarn" and
+    1 otherwise unless given.  `turns` are the frequencies as 64-bit fixed-point
+    turns per position (rotary_dim/2 Python integers)."""
+
+    def __init__(self, rotary_dim: int, base: float = 10000.0, kind: str = "plain", factor: float = 1.0,
+                 original_positions: float = 0, slow_turns: float = 1.0, fast_turns: Optional[float] = None,
+                 attention_factor: Optional[float] = None):
+        if kind not in _ROPE_KINDS:
+            raise MinisglError(f"kind must be one of {', '.join(_ROPE_KINDS)}, got {kind!r}")
+        if attention_factor is not None and not attention_factor > 0:
+            raise MinisglError("attention_factor must be positive")
+        if fast_turns is None:
+            fast_turns = 32.0 if kind == "yarn" else 4.0
+        rotary_dim = operator.index(rotary_dim)
+        desc = _RopeDesc(kind=_ROPE_KINDS[kind], rotary_dim=rotary_dim, base=base, factor=factor,
+                         original_positions=original_positions, slow_turns=slow_turns, fast_turns=fast_turns,
+                         attention_factor=attention_factor or 0.0)
+        turns, attention = (ctypes.c_uint64 * max(rotary_dim // 2, 1))(), ctypes.c_float()
+        _check(load_library().minisgl_rope_frequencies(ctypes.byref(desc), turns, ctypes.byref(attention)),
+               "rope_frequencies")
+        self.rotary_dim, self.attention_factor = rotary_dim, attention.value
+        self._turns = turns
+
+    @property
+    def turns(self) -> List[int]:
+        return list(self._turns)
+
+
+def minisgl_rope_table(rope: Rope, positions: torch.Tensor, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """[cos | sin] rows [n, rotary_dim] float32 for positions [n] (int32): the
+    cos_sin_cache of the rotary calls for positions 0, 1, 2, .., or a step's own
+    rows (pass the token's number as its position then)."""
+    dev = _at(positions, "positions", _I32)
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_rope_table(rope, positions, out)
+    _vec(positions, "positions", None, dev)
+    n, width = positions.numel(), rope.rotary_dim
+    if out is None:
+        out = _new((n, width), (width, 1), torch.float32)
+    else:
+        _at(out, "out", torch.float32, dev)
+        if out.shape != (n, width) or not out.is_contiguous():
+            raise MinisglError("out must be contiguous [n, rotary_dim] float32")
+    _check(load_library().minisgl_rope_table(rope._turns, rope.attention_factor, width, positions.data_ptr(), n,
+                                             out.data_ptr(), _raw_stream(dev)), "rope_table")
+    return out
+
+
+# --------------------------------------------------------------------------- #
+# the 8-bit pool
+# --------------------------------------------------------------------------- #
+class KVPoolFP8:
+    """A paged KV pool in 8 bits with a scale per block of tokens and head (the
+    format is in include/minisgl.h): `data` (2, L, R, H_kv, d), e4m3 elements as
+    float8_e4m3fn or their uint8 bytes, and `scales` uint8 (2, L, ceil(R / B),
+    H_kv), powers of two (x stands for 2^(x - 127)), with B = block_tokens rows
+    to a block: 1, 16, 32 or 64, dividing page_size.  The rows of a layer are
+    contiguous (H_kv, d), a block's scales contiguous and starting at a multiple
+    of 4 bytes with room up to the next one; the axes before them may have any
+    strides.  Caller-owned device memory (KVPoolFP8.zeros makes one)."""
+
+    def __init__(self, data: torch.Tensor, scales: torch.Tensor, page_size: int = 1, block_tokens: int = 1):
+        if data.dim() != 5 or data.shape[0] != 2:
+            raise MinisglError("pool data must have shape (2, L, R, H_kv, d)")
+        if data.dtype == torch.float8_e4m3fn:
+            data = data.view(torch.uint8)
+        _need(data, "pool data", torch.uint8)
+        _need(scales, "pool scales", torch.uint8)
+        if block_tokens not in (1, 16, 32, 64):
+            raise MinisglError("block_tokens must be 1, 16, 32 or 64")
+        if page_size < 1 or page_size % block_tokens:
+            raise MinisglError("page_size must be a multiple of block_tokens")
+        _, L, R, H, d = data.shape
+        if tuple(scales.shape) != (2, L, -(-R // block_tokens), H):
+            raise MinisglError("pool scales must have shape (2, L, ceil(R / block_tokens), H_kv)")
+        if scales.device != data.device:
+            raise MinisglError("pool data and scales on different devices")
+        if data.stride(4) != 1 or (H > 1 and data.stride(3) != d):
+            raise MinisglError("pool rows must be (H_kv, d) contiguous")
+        if H > 1 and scales.stride(3) != 1:
+            raise MinisglError("a block's scales must be contiguous")
+        # strides of axes of one element mean nothing
+        room = -(-H // 4) * 4
+        self.data, self.scales, self.page_size, self.block_tokens = data, scales, page_size, block_tokens
+        self.num_layers, self.num_rows, self.num_kv_heads, self.head_dim = L, R, H, d
+        last = sum((n - 1) * s for n, s in zip(scales.shape[:3], scales.stride()[:3])) + room
+        if scales.numel() and scales.storage_offset() + last > scales.untyped_storage().nbytes():
+            raise MinisglError("pool scales need room up to a multiple of 4 heads behind the last block")
+        self._desc_all = _PoolFP8Desc(
+            k_data=data.data_ptr(), v_data=data.data_ptr() + data.stride(0),
+            k_scale=scales.data_ptr(), v_scale=scales.data_ptr() + scales.stride(0),
+            data_layer_stride=data.stride(1) if L > 1 else 0,
+            data_row_stride=data.stride(2) if R > 1 else -(-H * d // 16) * 16,
+            scale_layer_stride=scales.stride(1) if L > 1 else 0,
+            scale_block_stride=scales.stride(2) if scales.shape[2] > 1 else room,
+            num_layers=L, num_rows=R, num_kv_heads=H, head_dim=d, page_size=page_size, block_tokens=block_tokens,
+            dtype=MINISGL_FP8)
+        self._ref = ctypes.byref(self._desc_all)
+        self._index = data.get_device()
+
+    @classmethod
+    def zeros(cls, num_layers: int, num_rows: int, num_kv_heads: int, head_dim: int, page_size: int = 1,
+              block_tokens: Optional[int] = None, device=None) -> "KVPoolFP8":
+        """A new pool; blocks of 16 rows where page_size allows, else of one."""
+        if block_tokens is None:
+            block_tokens = 16 if page_size % 16 == 0 else 1
+        device = device or "cuda"
+        scales = torch.zeros((2, num_layers, -(-num_rows // block_tokens), -(-num_kv_heads // 4) * 4),
+                             dtype=torch.uint8, device=device)
+        return cls(torch.zeros((2, num_layers, num_rows, num_kv_heads, head_dim), dtype=torch.uint8, device=device),
+                   scales[..., :num_kv_heads], page_size, block_tokens)
+
+    def _desc(self, layer: int):
+        if not 0 <= layer < self.num_layers:
+            raise MinisglError(f"layer {layer} outside [0, {self.num_layers})")
+        return self._ref
+
+
+def kv_pool_fp8_bytes(num_layers: int, num_kv_heads: int, head_dim: int, num_tokens: int,
+                      block_tokens: int = 16) -> int:
+    """Bytes an 8-bit pool needs to hold num_tokens token rows in every layer, K and V."""
+    blocks = -(-num_tokens // block_tokens)
+    return 2 * num_layers * (num_kv_heads * head_dim * num_tokens + -(-num_kv_heads // 4) * 4 * blocks)
+
+
+def minisgl_store_kv_fp8(pool: KVPoolFP8, layer: int, k: torch.Tensor, v: torch.Tensor, out_loc: torch.Tensor,
+                         stream=None) -> None:
+    """Quantise k[i], v[i] ([n_tokens, H_kv, d] bf16) into row out_loc[i] of the
+    8-bit pool.  The new rows of a block follow one another in out_loc (as
+    minisgl_build_slots lays them out)."""
+    dev, row = pool._index, pool.num_kv_heads * pool.head_dim
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_store_kv_fp8(pool, layer, k, v, out_loc)
+    n = out_loc.numel()
+    _vec(out_loc, "out_loc", None, dev)
+    ks, vs = _kv_rows(k, "k", n, row, dev), _kv_rows(v, "v", n, row, dev)
+    _check(load_library().minisgl_store_kv_fp8(pool._desc(layer), layer, k.data_ptr(), v.data_ptr(), ks, vs,
+                                               out_loc.data_ptr(), n, _raw_stream(dev)), "store_kv_fp8")
+
+
+def minisgl_rope_store_kv_fp8(pool: KVPoolFP8, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                              positions: torch.Tensor, cos_sin_cache: torch.Tensor, out_loc: torch.Tensor,
+                              interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """Rotate the first cos_sin_cache.shape[1] channels of the heads of q [N, H_q, d]
+    and k by each token's position, in half-split or interleaved pairs, and
+    quantise the rotated k, and v, into the 8-bit pool.  Returns the rotated q,
+    in q_out if given, else in q itself.  k is left unrotated."""
+    dev, d = pool._index, pool.head_dim
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_rope_store_kv_fp8(pool, layer, q, k, v, positions, cos_sin_cache, out_loc, interleaved,
+                                             q_out)
+    n, row = out_loc.numel(), pool.num_kv_heads * d
+    _vec(out_loc, "out_loc", None, dev)
+    _vec(positions, "positions", n, dev)
+    ks, vs = _kv_rows(k, "k", n, row, dev), _kv_rows(v, "v", n, row, dev)
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != n or shape[2] != d:
+        raise MinisglError("q must be [n_tokens, H_q, head_dim]")
+    q_row = shape[1] * d
+    qs = _kv_rows(q, "q", n, q_row, dev)
+    if q_out is None:
+        q_out, outs = q, qs
+    elif q_out.shape != shape:
+        raise MinisglError("q_out must have the shape of q")
+    else:
+        outs = _kv_rows(q_out, "q_out", n, q_row, dev)
+    _at(cos_sin_cache, "cos_sin_cache", torch.float32, dev)
+    if cos_sin_cache.dim() != 2 or not cos_sin_cache.is_contiguous():
+        raise MinisglError("cos_sin_cache must be contiguous [max_positions, rotary_dim] float32")
+    most, rotary = cos_sin_cache.shape
+    _check(load_library().minisgl_rope_store_kv_fp8(
+        pool._desc(layer), layer, q.data_ptr(), shape[1], qs, q_out.data_ptr(), outs, k.data_ptr(), v.data_ptr(), ks,
+        vs, positions.data_ptr(), cos_sin_cache.data_ptr(), most, rotary, 1 if interleaved else 0, out_loc.data_ptr(),
+        n, _raw_stream(dev)), "rope_store_kv_fp8")
+    return q_out
+
+
+def minisgl_load_kv_fp8(pool: KVPoolFP8, layer: int, page_table: torch.Tensor, lens: torch.Tensor,
+                        offsets: torch.Tensor, total_tokens: int, k_out: Optional[torch.Tensor] = None,
+                        v_out: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Rows page_table[r, :lens[r]] of the 8-bit pool as bf16, request r's from
+    row offsets[r] of k_out and v_out ([total_tokens, H_kv, d], made here if
+    not given; rows that no request fills are not written)."""
+    dev, H, d = pool._index, pool.num_kv_heads, pool.head_dim
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_load_kv_fp8(pool, layer, page_table, lens, offsets, total_tokens, k_out, v_out)
+    B, total = lens.numel(), int(total_tokens)
+    if total < 0:
+        raise MinisglError("total_tokens must not be negative")
+    stride, width = _table(page_table, B, dev)
+    _vec(lens, "lens", None, dev)
+    _vec(offsets, "offsets", B + 1, dev)
+    row = H * d
+    ks = row if k_out is None else _kv_rows(k_out, "k_out", total, row, dev, "total_tokens")
+    vs = row if v_out is None else _kv_rows(v_out, "v_out", total, row, dev, "total_tokens")
+    if k_out is None:
+        k_out = _new((total, H, d), (row, d, 1), _BF16)
+    if v_out is None:
+        v_out = _new((total, H, d), (row, d, 1), _BF16)
+    _check(load_library().minisgl_load_kv_fp8(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
+                                              lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
+                                              v_out.data_ptr(), ks, vs, _raw_stream(dev)), "load_kv_fp8")
+    return k_out, v_out
+
+
+def decode_workspace_fp8(batch: int, num_q_heads: int, pool: KVPoolFP8,
+                         max_splits: Optional[int] = None) -> torch.Tensor:
+    """A new workspace for minisgl_decode_attn_fp8 on the pool's device.  Calls
+    that may run at the same time need different ones.  max_splits (2 to 256):
+    the partial results that a request can have; unless given 32, and up to 256
+    for a few requests, which would leave most of the GPU idle with fewer."""
+    if max_splits is None:
+        max_splits = min(256, max(32, 1024 // max(batch, 1)))
+    return torch.empty(minisgl_decode_workspace_bytes(batch, num_q_heads, pool.num_kv_heads, pool.head_dim,
+                                                      max_splits), dtype=torch.uint8, device=pool.data.device)
+
+
+def minisgl_decode_attn_fp8(pool: KVPoolFP8, layer: int, q: torch.Tensor, page_table: torch.Tensor,
+                            seq_lens: torch.Tensor, sm_scale: float, out: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, split_tokens: int = 0,
+                            max_splits: Optional[int] = None, stream=None) -> torch.Tensor:
+    """Decode attention of q [B, H_q, d] over each request's page_table row of
+    the 8-bit pool.  Without a workspace the call allocates its own."""
+    dev = _at(q, "q", _BF16, pool._index)
+    if stream is not None or _device() != dev:
+        with _on(stream, dev):
+            return minisgl_decode_attn_fp8(pool, layer, q, page_table, seq_lens, sm_scale, out, workspace,
+                                           split_tokens, max_splits)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != pool.head_dim or not q.is_contiguous():
+        raise MinisglError("q must be contiguous [B, H_q, head_dim]")
+    B, Hq, d = shape
+    stride, width = _table(page_table, B, dev)
+    _vec(seq_lens, "seq_lens", B, dev)
+    if out is None:
+        out = _new((B, Hq, d), (Hq * d, d, 1), _BF16)
+    else:
+        _at(out, "out", _BF16, dev)
+        if out.shape != shape or not out.is_contiguous():
+            raise MinisglError("out must be contiguous with the shape of q")
+    if workspace is None:
+        workspace = decode_workspace_fp8(B, Hq, pool, max_splits)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise MinisglError("workspace must be a contiguous CUDA tensor on the pool's device")
+    _check(load_library().minisgl_decode_attn_fp8(
+        pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B, stride, width, seq_lens.data_ptr(),
+        float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, split_tokens,
+        _raw_stream(dev)), "decode_attn_fp8")
     return out

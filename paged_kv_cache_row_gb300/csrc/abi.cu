@@ -135,9 +135,11 @@ int minisgl_debug_timeout_count(uint32_t *count) {
     if (!count) return fail(MINISGL_ERR_ARG, "debug_timeout_count: NULL count");
     unsigned int c = 0;
     unsigned int d = 0;
+    unsigned int e = 0;
     if (int rc = cuda_status(minisgl::read_kernel_timeouts(&c), "debug_timeout_count")) return rc;
     if (int rc = cuda_status(minisgl::read_fp4_timeouts(&d), "debug_timeout_count")) return rc;
-    *count = c + d;
+    if (int rc = cuda_status(minisgl::read_fp8_timeouts(&e), "debug_timeout_count")) return rc;
+    *count = c + d + e;
     return MINISGL_OK;
 }
 
@@ -898,6 +900,278 @@ int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, cons
     if (batch == 0) return MINISGL_OK;
     a.pool = fp4_layer(pool, layer);
     return cuda_status(minisgl::launch_decode_fp4(a, static_cast<cudaStream_t>(stream)), "decode_attn_fp4");
+}
+
+}  // extern "C"
+
+namespace {
+
+int check_pool_fp8(const minisgl_kv_pool_fp8 *p, int32_t layer, const char *who) {
+    if (!p) return fail(MINISGL_ERR_ARG, "%s: pool descriptor is NULL", who);
+    if (p->dtype != MINISGL_FP8) return fail(MINISGL_ERR_DTYPE, "%s: pool dtype must be fp8", who);
+    if (!p->k_data || !p->v_data || !p->k_scale || !p->v_scale)
+        return fail(MINISGL_ERR_ARG, "%s: pool base is NULL", who);
+    if (p->head_dim != 64 && p->head_dim != 128)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: head_dim %d not in {64, 128}", who, p->head_dim);
+    if (p->num_kv_heads < 1 || p->num_rows < 1 || p->num_layers < 1)
+        return fail(MINISGL_ERR_SHAPE, "%s: pool sizes must be positive", who);
+    if (p->num_kv_heads > 4096)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: num_kv_heads %d > 4096", who, p->num_kv_heads);
+    if (p->block_tokens != 1 && p->block_tokens != 16 && p->block_tokens != 32 && p->block_tokens != 64)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: block_tokens %d not in {1, 16, 32, 64}", who, p->block_tokens);
+    if (p->page_size < 1 || p->page_size % p->block_tokens)
+        return fail(MINISGL_ERR_SHAPE, "%s: page_size %d is not a multiple of block_tokens %d", who, p->page_size,
+                    p->block_tokens);
+    if (p->data_row_stride < (int64_t)p->num_kv_heads * p->head_dim || p->data_row_stride % 16)
+        return fail(MINISGL_ERR_SHAPE, "%s: data_row_stride %lld must be >= H_kv*d and a multiple of 16", who,
+                    (long long)p->data_row_stride);
+    if (p->scale_block_stride < (p->num_kv_heads + 3) / 4 * 4 || p->scale_block_stride % 4)
+        return fail(MINISGL_ERR_SHAPE, "%s: scale_block_stride %lld must be a multiple of 4 and >= H_kv rounded up to one",
+                    who, (long long)p->scale_block_stride);
+    if (p->data_row_stride > INT32_MAX || p->scale_block_stride > INT32_MAX)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: strides of rows and blocks must be below 2^31 bytes", who);
+    if (!aligned16(p->k_data) || !aligned16(p->v_data) || p->data_layer_stride % 16)
+        return fail(MINISGL_ERR_SHAPE, "%s: data bases and strides must be multiples of 16 bytes", who);
+    if ((reinterpret_cast<uintptr_t>(p->k_scale) | reinterpret_cast<uintptr_t>(p->v_scale)) % 4 ||
+        p->scale_layer_stride % 4)
+        return fail(MINISGL_ERR_SHAPE, "%s: scale bases and strides must be multiples of 4 bytes", who);
+    if (layer < 0 || layer >= p->num_layers)
+        return fail(MINISGL_ERR_ARG, "%s: layer %d outside [0, %d)", who, layer, p->num_layers);
+    return MINISGL_OK;
+}
+
+minisgl::Fp8Layer fp8_layer(const minisgl_kv_pool_fp8 *p, int32_t layer) {
+    minisgl::Fp8Layer l;
+    l.k_data = static_cast<uint8_t *>(p->k_data) + layer * p->data_layer_stride;
+    l.v_data = static_cast<uint8_t *>(p->v_data) + layer * p->data_layer_stride;
+    l.k_scale = static_cast<uint8_t *>(p->k_scale) + layer * p->scale_layer_stride;
+    l.v_scale = static_cast<uint8_t *>(p->v_scale) + layer * p->scale_layer_stride;
+    l.data_stride = p->data_row_stride;
+    l.scale_stride = p->scale_block_stride;
+    l.num_rows = p->num_rows;
+    l.num_kv_heads = p->num_kv_heads;
+    l.head_dim = p->head_dim;
+    l.block_log2 = 0;
+    while ((1 << l.block_log2) < p->block_tokens) ++l.block_log2;
+    return l;
+}
+
+// The checks and arguments of both stores, without the rotation.
+int store_fp8_args(minisgl::StoreFp8Args &a, const char *who, const minisgl_kv_pool_fp8 *pool, int32_t layer,
+                   const void *k, const void *v, int64_t k_tok_stride, int64_t v_tok_stride, const int32_t *out_loc,
+                   int32_t n_tokens) {
+    if (int rc = check_pool_fp8(pool, layer, who)) return rc;
+    if (n_tokens < 0) return fail(MINISGL_ERR_ARG, "%s: n_tokens < 0", who);
+    a.n_tokens = n_tokens;
+    if (n_tokens == 0) return MINISGL_OK;
+    if (!k || !v || !out_loc) return fail(MINISGL_ERR_ARG, "%s: NULL k, v or out_loc", who);
+    const int64_t row = (int64_t)pool->num_kv_heads * pool->head_dim;
+    if (!aligned16(k) || !aligned16(v)) return fail(MINISGL_ERR_SHAPE, "%s: k and v must be 16-byte aligned", who);
+    if (k_tok_stride < row || v_tok_stride < row || k_tok_stride % 8 || v_tok_stride % 8)
+        return fail(MINISGL_ERR_SHAPE, "%s: token strides must be >= H_kv*d and multiples of 8", who);
+    if (n_tokens * (row / 8) >= (int64_t(1) << 31))
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: n_tokens * H_kv * d too large for one call", who);
+    a.pool = fp8_layer(pool, layer);
+    a.k = k;
+    a.v = v;
+    a.k_tok_stride = k_tok_stride;
+    a.v_tok_stride = v_tok_stride;
+    a.out_loc = out_loc;
+    a.rotary_dim = 0;
+    a.interleaved = false;
+    a.q = a.q_out = nullptr;
+    a.q_tok_stride = a.q_out_tok_stride = 0;
+    a.num_q_heads = 0;
+    a.positions = nullptr;
+    a.cos_sin = nullptr;
+    a.max_positions = 0;
+    return MINISGL_OK;
+}
+
+// Whether [a, a + na) and [b, b + nb) (in bytes) share memory.
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+}  // namespace
+
+extern "C" {
+
+int minisgl_rope_frequencies(const minisgl_rope *rope, uint64_t *turns, float *attention) {
+    g_err.clear();
+    if (!rope || !turns || !attention) return fail(MINISGL_ERR_ARG, "rope_frequencies: NULL argument");
+    const int n = rope->rotary_dim;
+    const double f = rope->factor, origin = rope->original_positions;
+    double base = rope->base;
+    if (n < 16 || n > minisgl::ROPE_MAX_DIM || n % 16)
+        return fail(MINISGL_ERR_UNSUPPORTED, "rope_frequencies: rotary_dim %d is not a multiple of 16 up to %d", n,
+                    minisgl::ROPE_MAX_DIM);
+    if (!(base > 1.0 && base <= 1e30)) return fail(MINISGL_ERR_ARG, "rope_frequencies: base must be in (1, 1e30]");
+    if (rope->kind < MINISGL_ROPE_PLAIN || rope->kind > MINISGL_ROPE_YARN)
+        return fail(MINISGL_ERR_ARG, "rope_frequencies: unknown kind %d", rope->kind);
+    if (rope->kind != MINISGL_ROPE_PLAIN && !(f >= 1.0 && f <= 1e6))
+        return fail(MINISGL_ERR_ARG, "rope_frequencies: factor must be in [1, 1e6]");
+    const bool bands = rope->kind == MINISGL_ROPE_BANDS, yarn = rope->kind == MINISGL_ROPE_YARN;
+    if ((bands || yarn) && !(origin >= 1.0 && origin <= 1e9))
+        return fail(MINISGL_ERR_ARG, "rope_frequencies: original_positions must be in [1, 1e9]");
+    if ((bands || yarn) && !(rope->slow_turns > 0.0 && rope->slow_turns < rope->fast_turns && rope->fast_turns <= 1e9))
+        return fail(MINISGL_ERR_ARG, "rope_frequencies: need 0 < slow_turns < fast_turns");
+    const double m = rope->attention_factor != 0.0 ? rope->attention_factor : yarn ? 0.1 * std::log(f) + 1.0 : 1.0;
+    if (!(m > 0.0 && m <= 1e6)) return fail(MINISGL_ERR_ARG, "rope_frequencies: attention_factor must be in [0, 1e6]");
+    const double tau = 6.283185307179586476925286766559;
+    if (rope->kind == MINISGL_ROPE_NTK) base *= std::pow(f, n / (n - 2.0));
+    double lo = 0.0, hi = 0.0;
+    if (yarn) {
+        lo = std::max(0.0, std::floor(n * std::log(origin / (rope->fast_turns * tau)) / (2 * std::log(base))));
+        hi = std::min(n - 1.0, std::ceil(n * std::log(origin / (rope->slow_turns * tau)) / (2 * std::log(base))));
+        if (hi <= lo) hi = lo + 0.001;
+    }
+    for (int j = 0; j < n / 2; ++j) {
+        double theta = std::pow(base, -2.0 * j / n);
+        double slow = rope->kind == MINISGL_ROPE_LINEAR ? 1.0 : 0.0;  // how far theta goes over to theta / f
+        if (bands)
+            slow = 1.0 - std::min(1.0, std::max(0.0, (origin * theta / tau - rope->slow_turns) /
+                                                         (rope->fast_turns - rope->slow_turns)));
+        if (yarn) slow = std::min(1.0, std::max(0.0, (j - lo) / (hi - lo)));
+        theta = slow * theta / f + (1.0 - slow) * theta;
+        turns[j] = (uint64_t)std::llrint(std::ldexp(theta / tau, 64));  // theta <= 1: below a sixth of 2^64
+    }
+    *attention = (float)m;
+    return MINISGL_OK;
+}
+
+int minisgl_rope_table(const uint64_t *turns, float attention, int32_t rotary_dim, const int32_t *positions, int32_t n,
+                       float *out, void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_rope_table");
+    if (!turns) return fail(MINISGL_ERR_ARG, "rope_table: NULL turns");
+    if (rotary_dim < 16 || rotary_dim > minisgl::ROPE_MAX_DIM || rotary_dim % 16)
+        return fail(MINISGL_ERR_UNSUPPORTED, "rope_table: rotary_dim %d is not a multiple of 16 up to %d", rotary_dim,
+                    minisgl::ROPE_MAX_DIM);
+    if (n < 0) return fail(MINISGL_ERR_ARG, "rope_table: n < 0");
+    if (n == 0) return MINISGL_OK;
+    if (!positions || !out) return fail(MINISGL_ERR_ARG, "rope_table: NULL positions or out");
+    if (!aligned16(out)) return fail(MINISGL_ERR_SHAPE, "rope_table: out must be 16-byte aligned");
+    if (overlap(positions, (int64_t)n * 4, out, (int64_t)n * rotary_dim * 4))
+        return fail(MINISGL_ERR_ARG, "rope_table: out overlaps positions");
+    minisgl::RopeTableArgs a = {};
+    std::copy(turns, turns + rotary_dim / 2, a.turns);
+    a.attention = attention;
+    a.rotary_dim = rotary_dim;
+    a.positions = positions;
+    a.n = n;
+    a.out = out;
+    return cuda_status(minisgl::launch_rope_table(a, static_cast<cudaStream_t>(stream)), "rope_table");
+}
+
+int minisgl_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const void *k, const void *v,
+                         int64_t k_tok_stride, int64_t v_tok_stride, const int32_t *out_loc, int32_t n_tokens,
+                         void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_store_kv_fp8");
+    minisgl::StoreFp8Args a;
+    if (int rc = store_fp8_args(a, "store_kv_fp8", pool, layer, k, v, k_tok_stride, v_tok_stride, out_loc, n_tokens))
+        return rc;
+    if (n_tokens == 0) return MINISGL_OK;
+    return cuda_status(minisgl::launch_store_kv_fp8(a, static_cast<cudaStream_t>(stream)), "store_kv_fp8");
+}
+
+int minisgl_rope_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                              int64_t q_tok_stride, void *q_out, int64_t q_out_tok_stride, const void *k,
+                              const void *v, int64_t k_tok_stride, int64_t v_tok_stride, const int32_t *positions,
+                              const float *cos_sin_cache, int32_t max_positions, int32_t rotary_dim,
+                              int32_t interleaved, const int32_t *out_loc, int32_t n_tokens, void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_rope_store_kv_fp8");
+    const char *who = "rope_store_kv_fp8";
+    minisgl::StoreFp8Args a;
+    if (int rc = store_fp8_args(a, who, pool, layer, k, v, k_tok_stride, v_tok_stride, out_loc, n_tokens)) return rc;
+    if (num_q_heads < 0 || max_positions < 1)
+        return fail(MINISGL_ERR_ARG, "%s: need num_q_heads >= 0 and max_positions >= 1", who);
+    if (rotary_dim < 16 || rotary_dim > pool->head_dim || rotary_dim % 16)
+        return fail(MINISGL_ERR_UNSUPPORTED, "%s: rotary_dim %d is not a multiple of 16 up to head_dim", who, rotary_dim);
+    if (n_tokens == 0) return MINISGL_OK;
+    if (!positions || !cos_sin_cache || (num_q_heads > 0 && (!q || !q_out)))
+        return fail(MINISGL_ERR_ARG, "%s: NULL q, q_out, positions or cos_sin_cache", who);
+    if (!aligned16(cos_sin_cache)) return fail(MINISGL_ERR_SHAPE, "%s: cos_sin_cache must be 16-byte aligned", who);
+    if (num_q_heads > 0) {
+        const int64_t row = (int64_t)num_q_heads * pool->head_dim;
+        if (!aligned16(q) || !aligned16(q_out))
+            return fail(MINISGL_ERR_SHAPE, "%s: q and q_out must be 16-byte aligned", who);
+        if (q_tok_stride < row || q_out_tok_stride < row || q_tok_stride % 8 || q_out_tok_stride % 8)
+            return fail(MINISGL_ERR_SHAPE, "%s: q's token strides must be >= H_q*d and multiples of 8", who);
+        if (n_tokens * (row / 8) >= (int64_t(1) << 31))
+            return fail(MINISGL_ERR_UNSUPPORTED, "%s: n_tokens * H_q * d too large for one call", who);
+        const bool in_place = q == q_out && q_tok_stride == q_out_tok_stride;
+        if (!in_place && overlap(q, ((n_tokens - 1) * q_tok_stride + row) * 2, q_out,
+                                 ((n_tokens - 1) * q_out_tok_stride + row) * 2))
+            return fail(MINISGL_ERR_ARG, "%s: q_out overlaps q without being q", who);
+    }
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved != 0;
+    a.q = q;
+    a.q_out = q_out;
+    a.q_tok_stride = q_tok_stride;
+    a.q_out_tok_stride = q_out_tok_stride;
+    a.num_q_heads = num_q_heads;
+    a.positions = positions;
+    a.cos_sin = cos_sin_cache;
+    a.max_positions = max_positions;
+    return cuda_status(minisgl::launch_store_kv_fp8(a, static_cast<cudaStream_t>(stream)), who);
+}
+
+int minisgl_load_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const int32_t *page_table, int32_t batch,
+                        int64_t pt_row_stride, int32_t pt_width, const int32_t *lens, const int32_t *offsets,
+                        int32_t total_tokens, void *k_out, void *v_out, int64_t k_tok_stride, int64_t v_tok_stride,
+                        void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_load_kv_fp8");
+    if (int rc = check_pool_fp8(pool, layer, "load_kv_fp8")) return rc;
+    if (batch < 0 || batch > 4096) return fail(MINISGL_ERR_ARG, "load_kv_fp8: batch %d outside [0, 4096]", batch);
+    if (total_tokens < 0) return fail(MINISGL_ERR_ARG, "load_kv_fp8: total_tokens < 0");
+    if (batch == 0 || total_tokens == 0) return MINISGL_OK;
+    if (!page_table || !lens || !offsets || !k_out || !v_out)
+        return fail(MINISGL_ERR_ARG, "load_kv_fp8: NULL pointer argument");
+    if (pt_width < 0 || pt_row_stride < pt_width)
+        return fail(MINISGL_ERR_SHAPE, "load_kv_fp8: need 0 <= pt_width <= pt_row_stride");
+    const int64_t row = (int64_t)pool->num_kv_heads * pool->head_dim;
+    if (!aligned16(k_out) || !aligned16(v_out))
+        return fail(MINISGL_ERR_SHAPE, "load_kv_fp8: k_out and v_out must be 16-byte aligned");
+    if (k_tok_stride < row || v_tok_stride < row || k_tok_stride % 8 || v_tok_stride % 8)
+        return fail(MINISGL_ERR_SHAPE, "load_kv_fp8: token strides must be >= H_kv*d and multiples of 8");
+    minisgl::LoadFp8Args a;
+    a.pool = fp8_layer(pool, layer);
+    a.page_table = page_table;
+    a.pt_stride = pt_row_stride;
+    a.pt_width = pt_width;
+    a.batch = batch;
+    a.lens = lens;
+    a.offsets = offsets;
+    a.total_tokens = total_tokens;
+    a.k_out = k_out;
+    a.v_out = v_out;
+    a.k_tok_stride = k_tok_stride;
+    a.v_tok_stride = v_tok_stride;
+    return cuda_status(minisgl::launch_load_kv_fp8(a, static_cast<cudaStream_t>(stream)), "load_kv_fp8");
+}
+
+int minisgl_decode_attn_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const void *q, int32_t num_q_heads,
+                            const int32_t *page_table, int32_t batch, int64_t pt_row_stride, int32_t pt_width,
+                            const int32_t *seq_lens, float sm_scale, void *out, void *workspace,
+                            size_t workspace_bytes, int32_t split_tokens, void *stream) {
+    g_err.clear();
+    NvtxRange nvtx_range("minisgl_decode_attn_fp8");
+    if (int rc = check_pool_fp8(pool, layer, "decode_attn_fp8")) return rc;
+    if (pt_width > SLOT_MAX) return fail(MINISGL_ERR_UNSUPPORTED, "decode_attn_fp8: pt_width above 2^30");
+    minisgl::DecodeFp8Args a;
+    if (int rc = decode_args(a.d, "decode_attn_fp8", pool->num_kv_heads, pool->head_dim, pool->num_rows, q,
+                             num_q_heads, page_table, batch, pt_row_stride, pt_width, seq_lens, sm_scale, out,
+                             workspace, workspace_bytes, split_tokens))
+        return rc;
+    if (batch == 0) return MINISGL_OK;
+    a.pool = fp8_layer(pool, layer);
+    return cuda_status(minisgl::launch_decode_fp8(a, static_cast<cudaStream_t>(stream)), "decode_attn_fp8");
 }
 
 }  // extern "C"

@@ -1,0 +1,294 @@
+// decode_fp8_kernel.cuh -- split-KV GQA decode attention over the 8-bit paged pool.
+//
+//     out[r,h] = sum_j softmax_j(sm_scale <q[r,h], K_j>) V_j,   j < seq_len[r],
+// K_j and V_j the values c * 2^e of row page_table[r, j] (the pool's format is
+// in the public header).  Split partials are merged by decode_merge_kernel.
+//
+// What bounds it: the K/V bytes, 2 d a token and KV head.
+//
+// Work: tiles of 32 tokens of one request and a block of up to 8 KV heads, one
+// warp to a head, so that a token's row of these heads (contiguous) is fetched
+// as one piece.  A CTA (one per SM) has as many such groups of warps as fit 8
+// warps (16 at d 64), each with a range of tiles of its own; the tiles of all
+// requests are cut evenly over the groups of all CTAs (split::Schedule).
+//
+// Loads: each group has a ring of three or more stages with a full and an
+// empty mbarrier each.  The group's warps fetch a tile together, each its run
+// of the tokens, in 16-byte cp.async pieces; a warp's own head's scales, one
+// byte of K and one of V per token, come as the 4-byte words that hold them.
+// Page-table entries are read a tile before the rows they name.  Rows past a
+// request's end repeat its last row; their weights are zero.
+#pragma once
+#include <algorithm>
+#include <cmath>
+
+#include "decode_fp4_plan.h"
+#include "decode_fp8.cuh"
+
+namespace minisgl {
+
+namespace {
+
+__device__ unsigned int fp8_timeouts = 0;  // one per translation unit
+
+using split::align_up;
+using split::cp_async_arrive;
+using split::Cursor;
+using split::guarded_wait;
+using split::ld_s32;
+using split::log2_up;
+using split::raise_limit;
+using split::row_at;
+using split::Schedule;
+using split::TILE;
+
+template <int D>
+constexpr int MAX_WARPS = D == 128 ? 8 : 16;
+constexpr int MAX_STAGES = 8;
+
+// How a CTA's warps and shared memory are laid out (set by the host).
+struct Layout {
+    int subs, hblocks, heads;   // groups of HEADS warps; head blocks and the heads of a full one
+    int stages;                 // of a ring
+    int whole;                  // a group takes whole streams, at most one each: no schedule, no merge
+    int off_bars, off_ring;
+};
+
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int D>
+constexpr int stage_bytes_of(int heads) {  // the tile's records, and 32 scale words of K and V for each head
+    return TILE * fp8::record_stride<D>(heads) + heads * TILE * 8;
+}
+
+}  // namespace
+
+// HEADS: warps of a group, a power of two; a head block has lay.heads of them at work.
+template <int D, int NG, int HEADS>
+__global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
+    decode_fp8_kernel(const DecodeFp8Args args, const float scale_log2, const Layout lay) {
+    using C = fp8::Head<D>;
+    const DecodeArgs &a = args.d;
+    const Fp8Layer &pool = args.pool;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_abort;
+    constexpr int stride = fp8::record_stride<D>(HEADS);
+    constexpr uint32_t stage_bytes = stage_bytes_of<D>(HEADS);
+    const int Hkv = a.num_kv_heads, Hq = a.num_q_heads, G = Hq / Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int stages = lay.stages;
+    const uint32_t data_stride = (uint32_t)pool.data_stride, scale_stride = (uint32_t)pool.scale_stride;
+
+    if ((int)threadIdx.x < lay.subs * stages) {  // full, empty of (ring, stage)
+        const uint32_t b = smem_u32(smem + lay.off_bars) + threadIdx.x * 16u;
+        mbar_init(b, 32u * HEADS);
+        mbar_init(b + 8u, HEADS);
+    }
+    if (threadIdx.x == 0) s_abort = 0;
+    fence_mbar_init();
+    pdl_wait();
+    pdl_launch_dependents();
+    Schedule sch;
+    sch.init(reinterpret_cast<int32_t *>(smem), a, lay.hblocks, (int)gridDim.x * lay.subs, lay.whole);
+    if (sch.total == 0) return;
+
+    // warp (sub, head): the ring of its group
+    const int head_in = warp % HEADS, sub = warp / HEADS;
+    const uint32_t bars = smem_u32(smem + lay.off_bars) + (uint32_t)(sub * stages) * 16u;
+    const uint32_t ring = smem_u32(smem + lay.off_ring) + (uint32_t)(sub * stages) * stage_bytes;
+    constexpr int v_off = HEADS * D, s_off = TILE * stride;
+
+    // This warp fetches tokens head_in * MINE .. of a tile; lane i holds the
+    // page-table entry of the tile's token i (past the end: the last one's).
+    constexpr int MINE = TILE / HEADS;
+    const int32_t *table = nullptr;  // entry of the first token of the tile to fetch
+    auto load_row = [&](int left) -> int { return ld_s32(table + min(lane, left - 1)); };
+    // A token's K (or V) row of HEADS heads is PIECES 16-byte pieces: one
+    // instruction copies 32 of them, or all pieces of several tokens.
+    constexpr int PIECES = HEADS * D / 16, ROUNDS = PIECES > 32 ? PIECES / 32 : 1;
+    constexpr int TOKS = PIECES < 32 ? 32 / PIECES : 1;
+    const int piece = lane % (PIECES < 32 ? PIECES : 32), sub_tok = lane / (PIECES < 32 ? PIECES : 32);
+    uint32_t in_at = 0, in_parity = 1;  // stage to fill; the first round finds every stage empty
+    auto issue = [&](int hb, int raw) {
+        const int row = min(max(raw, 0), a.num_rows - 1);
+        const uint32_t bar = bars + in_at * 16u, to = ring + in_at * stage_bytes;
+        const int h0 = hb * lay.heads, nh = min(lay.heads, Hkv - h0);
+        guarded_wait(bar + 8u, in_parity, &s_abort, &fp8_timeouts);
+        const uint8_t *ksrc = pool.k_data + h0 * D + piece * 16, *vsrc = pool.v_data + h0 * D + piece * 16;
+#pragma unroll
+        for (int i0 = 0; i0 < MINE; i0 += TOKS) {
+            const int tok = head_in * MINE + i0 + sub_tok;
+            const uint32_t e = __shfl_sync(0xffffffffu, row, tok);
+            const uint32_t dst = to + fp8::slot<D>(tok) * stride + piece * 16;
+            const uint8_t *k = row_at(ksrc, e, data_stride), *v = row_at(vsrc, e, data_stride);
+#pragma unroll
+            for (int j = 0; j < ROUNDS; ++j)
+                if (piece * 16 + j * 512 < nh * D) {
+                    cp_async_16(dst + j * 512, k + j * 512, 16);
+                    cp_async_16(dst + v_off + j * 512, v + j * 512, 16);
+                }
+        }
+        if (head_in < nh) {
+            const uint32_t blk = (uint32_t)row >> pool.block_log2, word = (uint32_t)(h0 + head_in) & ~3u;
+            const uint32_t dst = to + s_off + head_in * (TILE * 8) + lane * 8;
+            cp_async_4(dst, row_at(pool.k_scale + word, blk, scale_stride));
+            cp_async_4(dst + 4, row_at(pool.v_scale + word, blk, scale_stride));
+        }
+        cp_async_arrive(bar);
+        if (++in_at == (uint32_t)stages) {
+            in_at = 0;
+            in_parity ^= 1;
+        }
+    };
+
+    fp8::Stream<D, NG> w;
+    uint32_t at = 0, parity = 0;  // stage to use
+    // where the lane reads in the first stage: K of token lane / 4, the scale
+    // words, V of tokens 2 (lane % 4) and the next
+    const int lg = lane >> 2, lt = lane & 3;
+    const uint32_t rd_k = ring + head_in * D + fp8::slot<D>(lg) * stride + lt * C::QPT;
+    const uint32_t rd_s = ring + s_off + head_in * (TILE * 8);
+    const uint32_t rd_v0 = ring + v_off + head_in * D + fp8::slot<D>(2 * lt) * stride + lg * C::OPT;
+    const uint32_t rd_v1 = ring + v_off + head_in * D + fp8::slot<D>(2 * lt + 1) * stride + lg * C::OPT;
+    const int seg_step = (int)gridDim.x * lay.subs;
+    // neighbouring ranges on different SMs: few ranges spread over all of them
+    for (int seg = blockIdx.x + sub * (int)gridDim.x; seg < sch.nseg; seg += seg_step) {
+        Cursor c, pc;  // the tile to use, the tile to fetch
+        int use = sch.range(seg, c);  // tiles not used yet
+        if (use == 0) {  // a whole stream without context: zeros
+            const int head = c.hb * lay.heads + head_in;
+            if (head_in < lay.heads && head < Hkv)
+                for (int i = lane; i < G * D / 8; i += 32)
+                    st_v4(static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)c.r * Hq + head * G) * D + i * 8,
+                          make_uint4(0u, 0u, 0u, 0u));
+            continue;
+        }
+        // The tiles to fetch are those of pc until left reaches `stop`, then
+        // `later` more of the streams behind it.
+        pc = c;
+        int stop, later = use;
+        auto enter = [&]() {
+            table = a.page_table + (int64_t)pc.r * a.pt_stride + (sch.len(pc.r) - pc.left);
+            const int n = min(later, (pc.left + TILE - 1) / TILE);
+            stop = pc.left - n * TILE;
+            later -= n;
+        };
+        auto advance = [&]() -> int {  // the next tile to fetch; its page-table entry
+            pc.left -= TILE;
+            table += TILE;
+            if (pc.left <= stop && later > 0) {
+                sch.next_stream(pc);
+                enter();
+                // its queries, wanted when this tile is used
+                const int head = pc.hb * lay.heads + head_in;
+                w.prefetch(a, (int64_t)pc.r * Hq + head * G, G, head_in < lay.heads && head < Hkv, lane);
+            }
+            return pc.left > stop ? load_row(pc.left) : 0;
+        };
+        enter();
+        // the first two tiles' page-table entries at once, then one tile ahead
+        int row = load_row(pc.left);
+        for (int i = 0; i < stages - 1 && pc.left > stop; ++i) {
+            const int now = row, now_hb = pc.hb;
+            row = advance();
+            issue(now_hb, now);
+        }
+        bool from_start = c.left == sch.len(c.r);
+        // which of its stream's partials the range begins with (later streams begin here)
+        int split = from_start ? 0 : seg - sch.range_of(sch.before(c.r, c.hb));
+        while (use > 0) {  // a stream, or the range's part of it
+            const int head = c.hb * lay.heads + head_in;
+            const bool live = head_in < lay.heads && head < Hkv;
+            const int shift = (head & 3) * 8;
+            w.open(live ? static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)c.r * Hq + head * G) * D : nullptr, G,
+                   scale_log2, lane);
+            const int n = min(use, (c.left + TILE - 1) / TILE), end = c.left - n * TILE;
+            use -= n;
+            for (; c.left > end; c.left -= TILE) {
+                guarded_wait(bars + at * 16u, parity, &s_abort, &fp8_timeouts);
+                const uint32_t st = at * stage_bytes;
+                uint32_t pb[2][NG][2];
+                if (live) {
+                    w.scores(rd_k + st, rd_s + st, shift, stride, c.left, lane, pb);
+                    w.values(rd_v0 + st, rd_v1 + st, stride, pb);
+                }
+                if (pc.left > stop) {  // into the stage of the tile before this one
+                    issue(pc.hb, row);
+                    row = advance();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars + at * 16u + 8u);
+                if (++at == (uint32_t)stages) {
+                    at = 0;
+                    parity ^= 1;
+                }
+            }
+            const bool last = c.left <= 0;
+            if (live) {
+                w.close(a, (int64_t)c.r * Hq + head * G, G, from_start && last, split, lane);
+                if (last && lane == 0 && !sch.whole) a.split_count[(int64_t)c.r * Hkv + head] = split + 1;
+            }
+            if (use > 0) sch.next_stream(c);
+            from_start = true;
+            split = 0;
+        }
+    }
+    cp_async_wait<0>();  // nothing in flight when the CTA ends, even after a wait that ran out
+}
+
+namespace {
+
+template <int D, int NG, int HEADS>
+cudaError_t launch_cfg(const DecodeFp8Args &args, cudaStream_t s) {
+    const DecodeArgs &a = args.d;
+    Layout lay;
+    lay.heads = fp4::block_heads(a.num_kv_heads);
+    lay.hblocks = (a.num_kv_heads + lay.heads - 1) / lay.heads;
+    auto kern = decode_fp8_kernel<D, NG, HEADS>;
+    int optin = 0;
+    cudaError_t e = raise_limit(kern, optin);
+    if (e != cudaSuccess) return e;
+    // as many groups as leave three stages to each
+    constexpr int stage = stage_bytes_of<D>(HEADS);
+    lay.subs = MAX_WARPS<D> / HEADS;
+    lay.off_bars = align_up(split::schedule_ints(a.batch) * 4, 16);
+    lay.off_ring = align_up(lay.off_bars + MAX_STAGES * lay.subs * 16, 128);
+    lay.subs = std::min(lay.subs, (optin - lay.off_ring) / (3 * stage));
+    if (lay.subs < 1) return cudaErrorInvalidConfiguration;
+    lay.stages = std::min((optin - lay.off_ring) / (lay.subs * stage), MAX_STAGES);
+    const size_t smem = (size_t)lay.off_ring + (size_t)lay.stages * lay.subs * stage;
+    const int64_t sms = device_sm_count(), streams = (int64_t)a.batch * lay.hblocks;
+    const int64_t wide = (a.pt_width + TILE - 1) / TILE;
+    lay.whole = fp4::leave_whole(streams, sms * lay.subs, wide) && a.split_tokens == 0;
+    // never more ranges than tiles could exist
+    const int64_t max_tiles = streams * wide;
+    const int64_t grid = std::max<int64_t>(1, std::min(sms, lay.whole ? streams : max_tiles));
+    e = launch_pdl(kern, dim3((unsigned)grid), dim3(HEADS * lay.subs * 32), smem, s, args,
+                   a.sm_scale * split::LOG2E, lay);
+    if (e != cudaSuccess || lay.whole) return e;
+    const int64_t rows = (int64_t)a.batch * a.num_q_heads;  // up to 4 CTAs of 4 an SM: the wide form
+    return launch_pdl(rows <= 16 * sms ? split::decode_merge_kernel<D, 16> : split::decode_merge_kernel<D, 4>,
+                      dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a);
+}
+
+}  // namespace
+
+template <int D, int NG>
+cudaError_t launch_decode_fp8_as(const DecodeFp8Args &a, cudaStream_t s) {
+    switch (fp4::block_heads(a.d.num_kv_heads)) {
+        case 1: return launch_cfg<D, NG, 1>(a, s);
+        case 2: return launch_cfg<D, NG, 2>(a, s);
+        case 3:
+        case 4: return launch_cfg<D, NG, 4>(a, s);
+        default: return launch_cfg<D, NG, 8>(a, s);
+    }
+}
+
+template <int D, int NG>
+cudaError_t read_fp8_timeouts_as(unsigned int *count) {
+    return cudaMemcpyFromSymbol(count, fp8_timeouts, sizeof(unsigned int));
+}
+
+}  // namespace minisgl

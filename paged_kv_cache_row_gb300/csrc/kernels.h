@@ -215,6 +215,62 @@ struct DecodeFp4Args {
 };
 cudaError_t launch_decode_fp4(const DecodeFp4Args &a, cudaStream_t s);
 
+// One layer of an 8-bit pool: e4m3 elements and a power of two for each block
+// of 2^block_log2 rows and head, strides in bytes.
+struct Fp8Layer {
+    uint8_t *k_data, *v_data, *k_scale, *v_scale;
+    int64_t data_stride, scale_stride;  // between rows, between blocks
+    int32_t num_rows, num_kv_heads, head_dim, block_log2;
+};
+
+struct StoreFp8Args {
+    Fp8Layer pool;
+    const void *k, *v;            // bf16 rows
+    int64_t k_tok_stride, v_tok_stride;
+    const int32_t *out_loc;
+    int32_t n_tokens;
+    // the rotation (rotary_dim 0: none, and no q)
+    int32_t rotary_dim;
+    bool interleaved;
+    const void *q;                // bf16 [N, H_q, D], to q_out (which may be q)
+    void *q_out;
+    int64_t q_tok_stride, q_out_tok_stride;
+    int32_t num_q_heads;
+    const int32_t *positions;
+    const float *cos_sin;         // [max_positions, rotary_dim]: cos | sin
+    int32_t max_positions;
+};
+cudaError_t launch_store_kv_fp8(const StoreFp8Args &a, cudaStream_t s);
+
+struct LoadFp8Args {
+    Fp8Layer pool;
+    const int32_t *page_table;
+    int64_t pt_stride;
+    int32_t pt_width, batch;
+    const int32_t *lens, *offsets;  // [batch], [batch + 1]
+    int32_t total_tokens;
+    void *k_out, *v_out;          // bf16 rows
+    int64_t k_tok_stride, v_tok_stride;
+};
+cudaError_t launch_load_kv_fp8(const LoadFp8Args &a, cudaStream_t s);
+
+struct DecodeFp8Args {
+    DecodeArgs d;                 // k_layer, v_layer, row_stride unused
+    Fp8Layer pool;
+};
+cudaError_t launch_decode_fp8(const DecodeFp8Args &a, cudaStream_t s);
+
+constexpr int ROPE_MAX_DIM = 256;
+struct RopeTableArgs {
+    uint64_t turns[ROPE_MAX_DIM / 2];  // per frequency, turns per position * 2^64
+    float attention;              // factor of cos and sin
+    int32_t rotary_dim;
+    const int32_t *positions;     // [n]
+    int32_t n;
+    float *out;                   // [n, rotary_dim]
+};
+cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t s);
+
 int device_sm_count();
 
 // Sets the calling thread's minisgl_last_error() message and returns `code`.
@@ -223,7 +279,8 @@ int report_error(int code, const char *msg);
 // Number of bounded waits that ran out in tensor-core kernels since load
 // (synchronous copy from a device counter).
 cudaError_t read_kernel_timeouts(unsigned int *count);
-// The same for the 4-bit decode kernel.
+// The same for the 4-bit and 8-bit decode kernels.
 cudaError_t read_fp4_timeouts(unsigned int *count);
+cudaError_t read_fp8_timeouts(unsigned int *count);
 
 }  // namespace minisgl
