@@ -23,6 +23,7 @@ namespace minisgl {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int RESIDENT = 8;  // blocks per SM
 
 // cos and sin of phase / 2^64 turns
 __device__ __forceinline__ void cos_sin_of(uint64_t phase, float &c, float &s) {
@@ -43,15 +44,19 @@ __device__ __forceinline__ void cos_sin_of(uint64_t phase, float &c, float &s) {
 }  // namespace
 
 // h / 4 threads a position (h = rotary_dim / 2), `rows` positions a block at a time.
-__global__ void __launch_bounds__(THREADS) rope_table_kernel(const __grid_constant__ RopeTableArgs a, int rows) {
+__global__ void __launch_bounds__(THREADS, RESIDENT) rope_table_kernel(const __grid_constant__ RopeTableArgs a, int rows) {
+    // through shared memory: lanes that read parameters at different places do so one after the other
+    __shared__ uint64_t s_turns[ROPE_MAX_DIM / 2];
+    const int h = a.rotary_dim / 2, per_row = h / 4;
+    if ((int)threadIdx.x < h) s_turns[threadIdx.x] = a.turns[threadIdx.x];
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
-    const int h = a.rotary_dim / 2, per_row = h / 4;
     const int sub = threadIdx.x / per_row, j = (threadIdx.x - sub * per_row) * 4;
     if (sub >= rows) return;
     uint64_t f[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) f[k] = a.turns[j + k];
+    for (int k = 0; k < 4; ++k) f[k] = s_turns[j + k];
     for (int64_t i = (int64_t)blockIdx.x * rows + sub; i < a.n; i += (int64_t)gridDim.x * rows) {
         const uint64_t p = (uint64_t)(int64_t)a.positions[i];
         float c[4], s[4];
@@ -70,7 +75,7 @@ __global__ void __launch_bounds__(THREADS) rope_table_kernel(const __grid_consta
 cudaError_t launch_rope_table(const RopeTableArgs &a, cudaStream_t s) {
     if (a.n == 0) return cudaSuccess;
     const int rows = THREADS / (a.rotary_dim / 8);
-    const int64_t blocks = std::min<int64_t>(((int64_t)a.n + rows - 1) / rows, (int64_t)device_sm_count() * 16);
+    const int64_t blocks = std::min<int64_t>(((int64_t)a.n + rows - 1) / rows, (int64_t)device_sm_count() * RESIDENT);
     return launch_pdl(rope_table_kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, rows);
 }
 
