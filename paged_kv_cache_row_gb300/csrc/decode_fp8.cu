@@ -1,7 +1,7 @@
 // decode_fp8.cu -- decode attention over the 8-bit pool: the choice of kernel.
 //
 // The kernels (decode_fp8_kernel.cuh) are compiled in one file per head_dim
-// and number of 8-head query tiles, each for 1, 2, 4 and 8 warps of KV heads.
+// and number of 8-head query tiles, each for every size of a block of KV heads.
 #include "kernels.h"
 
 namespace minisgl {

@@ -2,15 +2,20 @@
 //
 //     out[r,h] = sum_j softmax_j(sm_scale <q[r,h], K_j>) V_j,   j < seq_len[r],
 // K_j and V_j the values c * 2^e of row page_table[r, j] (the pool's format is
-// in the public header).  Split partials are merged by decode_merge_kernel.
+// in the public header).  Split partials are joined by merge_rows_kernel or merge_row_kernel.
 //
 // What bounds it: the K/V bytes, 2 d a token and KV head.
 //
-// Work: tiles of 32 tokens of one request and a block of up to 8 KV heads, one
-// warp to a head, so that a token's row of these heads (contiguous) is fetched
-// as one piece.  A CTA (one per SM) has as many such groups of warps as fit 8
-// warps (16 at d 64), each with a range of tiles of its own; the tiles of all
-// requests are cut evenly over the groups of all CTAs (split::Schedule).
+// Work: tiles of 32 tokens of one request and a block of KV heads, one warp to a
+// head, so that a token's row of these heads (contiguous) is fetched as one
+// piece of up to 512 bytes.  A CTA (one per SM) has as many such groups of warps
+// as fit 8 warps (16 at d 64), each with a range of tiles of its own; the tiles
+// of all requests are cut evenly over the groups of all CTAs (split::Schedule).
+// At d 128, 8 heads, blocks of 4 make two groups, which load and compute in turns
+// of their own: 256 requests 224 us and 64 requests 58, where one block of 8
+// takes 228 and 60; blocks of 2 and of 1 make more partials and shorter copies
+// (230 and 253, 73 and 82).  At d 64 a block of 5, 6 or 7 heads takes 61, 62 and
+// 60 us where two blocks take 68, 66 and 65.
 //
 // Loads: each group has a ring of three or more stages with a full and an
 // empty mbarrier each.  The group's warps fetch a tile together, each its run
@@ -26,6 +31,19 @@
 #include "decode_fp8.cuh"
 
 namespace minisgl {
+namespace fp8 {
+
+// KV heads of a block: blocks of one size, the last with what is left, of up to
+// 512 bytes a row.
+template <int D>
+constexpr int MOST_HEADS = 512 / D;
+template <int D>
+constexpr int block_heads(int num_kv_heads) {
+    const int blocks = (num_kv_heads + MOST_HEADS<D> - 1) / MOST_HEADS<D>;
+    return (num_kv_heads + blocks - 1) / blocks;
+}
+
+}  // namespace fp8
 
 namespace {
 
@@ -48,7 +66,7 @@ constexpr int MAX_STAGES = 8;
 
 // How a CTA's warps and shared memory are laid out (set by the host).
 struct Layout {
-    int subs, hblocks, heads;   // groups of HEADS warps; head blocks and the heads of a full one
+    int subs, hblocks;          // groups of HEADS warps, head blocks
     int stages;                 // of a ring
     int whole;                  // a group takes whole streams, at most one each: no schedule, no merge
     int off_bars, off_ring;
@@ -65,7 +83,7 @@ constexpr int stage_bytes_of(int heads) {  // the tile's records, and 32 scale w
 
 }  // namespace
 
-// HEADS: warps of a group, a power of two; a head block has lay.heads of them at work.
+// HEADS: KV heads of a head block, one warp each (the last block may have fewer).
 template <int D, int NG, int HEADS>
 __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
     decode_fp8_kernel(const DecodeFp8Args args, const float scale_log2, const Layout lay) {
@@ -100,35 +118,32 @@ __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
     const uint32_t ring = smem_u32(smem + lay.off_ring) + (uint32_t)(sub * stages) * stage_bytes;
     constexpr int v_off = HEADS * D, s_off = TILE * stride;
 
-    // This warp fetches tokens head_in * MINE .. of a tile; lane i holds the
-    // page-table entry of the tile's token i (past the end: the last one's).
-    constexpr int MINE = TILE / HEADS;
+    // This warp fetches tokens head_in * MINE .. of a tile (the last warp of three
+    // fewer); lane i holds the page-table entry of the tile's token i (past the end:
+    // the last one's).
+    constexpr int MINE = (TILE + HEADS - 1) / HEADS;
     const int32_t *table = nullptr;  // entry of the first token of the tile to fetch
     auto load_row = [&](int left) -> int { return ld_s32(table + min(lane, left - 1)); };
-    // A token's K (or V) row of HEADS heads is PIECES 16-byte pieces: one
-    // instruction copies 32 of them, or all pieces of several tokens.
-    constexpr int PIECES = HEADS * D / 16, ROUNDS = PIECES > 32 ? PIECES / 32 : 1;
-    constexpr int TOKS = PIECES < 32 ? 32 / PIECES : 1;
-    const int piece = lane % (PIECES < 32 ? PIECES : 32), sub_tok = lane / (PIECES < 32 ? PIECES : 32);
+    // A token's K (or V) row of HEADS heads is up to 32 pieces of 16 bytes: one
+    // instruction copies them, or those of several tokens.
+    constexpr int LANES = 1 << log2_up(HEADS * D / 16), TOKS = 32 / LANES;
+    const int piece = lane % LANES, sub_tok = lane / LANES;
     uint32_t in_at = 0, in_parity = 1;  // stage to fill; the first round finds every stage empty
     auto issue = [&](int hb, int raw) {
         const int row = min(max(raw, 0), a.num_rows - 1);
         const uint32_t bar = bars + in_at * 16u, to = ring + in_at * stage_bytes;
-        const int h0 = hb * lay.heads, nh = min(lay.heads, Hkv - h0);
+        const int h0 = hb * HEADS, nh = min(HEADS, Hkv - h0);
         guarded_wait(bar + 8u, in_parity, &s_abort, &fp8_timeouts);
         const uint8_t *ksrc = pool.k_data + h0 * D + piece * 16, *vsrc = pool.v_data + h0 * D + piece * 16;
 #pragma unroll
         for (int i0 = 0; i0 < MINE; i0 += TOKS) {
-            const int tok = head_in * MINE + i0 + sub_tok;
-            const uint32_t e = __shfl_sync(0xffffffffu, row, tok);
+            const int i = i0 + sub_tok, tok = head_in * MINE + i;
+            const uint32_t e = __shfl_sync(0xffffffffu, row, tok & 31);
             const uint32_t dst = to + fp8::slot<D>(tok) * stride + piece * 16;
-            const uint8_t *k = row_at(ksrc, e, data_stride), *v = row_at(vsrc, e, data_stride);
-#pragma unroll
-            for (int j = 0; j < ROUNDS; ++j)
-                if (piece * 16 + j * 512 < nh * D) {
-                    cp_async_16(dst + j * 512, k + j * 512, 16);
-                    cp_async_16(dst + v_off + j * 512, v + j * 512, 16);
-                }
+            if (piece * 16 < nh * D && (TILE % HEADS == 0 || (i < MINE && tok < TILE))) {
+                cp_async_16(dst, row_at(ksrc, e, data_stride), 16);
+                cp_async_16(dst + v_off, row_at(vsrc, e, data_stride), 16);
+            }
         }
         if (head_in < nh) {
             const uint32_t blk = (uint32_t)row >> pool.block_log2, word = (uint32_t)(h0 + head_in) & ~3u;
@@ -158,8 +173,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
         Cursor c, pc;  // the tile to use, the tile to fetch
         int use = sch.range(seg, c);  // tiles not used yet
         if (use == 0) {  // a whole stream without context: zeros
-            const int head = c.hb * lay.heads + head_in;
-            if (head_in < lay.heads && head < Hkv)
+            const int head = c.hb * HEADS + head_in;
+            if (head < Hkv)
                 for (int i = lane; i < G * D / 8; i += 32)
                     st_v4(static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)c.r * Hq + head * G) * D + i * 8,
                           make_uint4(0u, 0u, 0u, 0u));
@@ -182,8 +197,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
                 sch.next_stream(pc);
                 enter();
                 // its queries, wanted when this tile is used
-                const int head = pc.hb * lay.heads + head_in;
-                w.prefetch(a, (int64_t)pc.r * Hq + head * G, G, head_in < lay.heads && head < Hkv, lane);
+                const int head = pc.hb * HEADS + head_in;
+                w.prefetch(a, (int64_t)pc.r * Hq + head * G, G, head < Hkv, lane);
             }
             return pc.left > stop ? load_row(pc.left) : 0;
         };
@@ -199,8 +214,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
         // which of its stream's partials the range begins with (later streams begin here)
         int split = from_start ? 0 : seg - sch.range_of(sch.before(c.r, c.hb));
         while (use > 0) {  // a stream, or the range's part of it
-            const int head = c.hb * lay.heads + head_in;
-            const bool live = head_in < lay.heads && head < Hkv;
+            const int head = c.hb * HEADS + head_in;
+            const bool live = head < Hkv;
             const int shift = (head & 3) * 8;
             w.open(live ? static_cast<const __nv_bfloat16 *>(a.q) + ((int64_t)c.r * Hq + head * G) * D : nullptr, G,
                    scale_log2, lane);
@@ -240,12 +255,179 @@ __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
 
 namespace {
 
+// The partials of the streams that were cut, joined: out = sum_k w_k O_k / sum_k
+// w_k, w_k = e^(LSE_k - max LSE).  Rows that are whole hold their output already;
+// empty requests get zeros.  Two kernels for the two ways a call is cut.  What
+// bounds both are rounds of dependent loads, about 1 us each behind the launch:
+// there are two, the counts with the first LSEs (read before it is known how many
+// count) and the partials.
+template <int D>
+struct Acc {
+    static constexpr int CPL = D / 32;  // channels per lane
+    float c[CPL];
+    __device__ __forceinline__ void load(const float *row, int lane) {
+        if constexpr (CPL == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + lane * 4);
+            c[0] = v.x, c[1] = v.y, c[2] = v.z, c[3] = v.w;
+        } else {
+            const float2 v = *reinterpret_cast<const float2 *>(row + lane * 2);
+            c[0] = v.x, c[1] = v.y;
+        }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) c[i] = 0.f;
+    }
+    __device__ __forceinline__ void add(const Acc &x, float w) {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) c[i] += w * x.c[i];
+    }
+    __device__ __forceinline__ void write(void *out, int64_t row, int lane, float scale) const {
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(out) + row * D + lane * CPL;
+#pragma unroll
+        for (int i = 0; i < CPL; i += 2)
+            *reinterpret_cast<uint32_t *>(dst + i) = pack_bf16x2(c[i] * scale, c[i + 1] * scale);
+    }
+};
+
+__device__ __forceinline__ int partials_of(const DecodeArgs &a, int row) {
+    const int r = row / a.num_q_heads, g = (row - r * a.num_q_heads) / (a.num_q_heads / a.num_kv_heads);
+    const int len = a.seq_lens[r], cnt = a.split_count[(int64_t)r * a.num_kv_heads + g];
+    return split::clamp_len(len, a.pt_width) == 0 ? 0 : min(cnt, a.max_splits);  // no count without context
+}
+
+// Many rows of a few partials: a warp takes 2 rows, all their loads under way
+// together (lane 16 i + k has the LSE of partial k of row i).  1024 rows in 3
+// partials take 2.9 us behind the kernel before, 4 rows to a warp 5.7; 8192 rows
+// 4.8 either way.
+constexpr int MERGE_THREADS = 128, MERGE_ROWS = 2;
+constexpr int MERGE_MANY = 4;  // ranges to a stream from which on a block takes a row
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_rows_kernel(const DecodeArgs a) {
+    constexpr int ROWS = MERGE_ROWS, MOST = 8, LANES = 32 / ROWS;  // rows, partials of one in flight, lanes of a row's LSEs
+    const int rows = a.batch * a.num_q_heads, lane = threadIdx.x & 31, k = lane % LANES;
+    const int row0 = (blockIdx.x * (MERGE_THREADS / 32) + (threadIdx.x >> 5)) * ROWS;
+    pdl_wait();
+    pdl_launch_dependents();
+    if (row0 >= rows) return;
+    const int mine = min(row0 + lane / LANES, rows - 1);
+    const float *lse = a.ws_lse + (int64_t)mine * a.max_splits;
+    const float l0 = k < a.max_splits ? lse[k] : 0.f;
+    const int n = partials_of(a, mine);
+    if (__all_sync(0xffffffffu, n == 1)) return;
+    float top = k < n ? l0 : -INFINITY;
+    for (int s = k + LANES; s < n; s += LANES) top = fmaxf(top, lse[s]);
+#pragma unroll
+    for (int o = 1; o < LANES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float w0 = k < n ? __expf(l0 - top) : 0.f;
+    int cnt[ROWS];
+    Acc<D> x[ROWS][MOST];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        cnt[i] = row0 + i < rows ? __shfl_sync(0xffffffffu, n, LANES * i) : 1;
+        const float *o = a.ws_o + (int64_t)(row0 + i) * a.max_splits * D;
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (cnt[i] > 1 && j < cnt[i]) x[i][j].load(o + j * D, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        Acc<D> acc;
+        acc.clear();
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < MOST; ++j) {
+            const float w = __shfl_sync(0xffffffffu, w0, LANES * i + j);
+            if (j < cnt[i]) {
+                sum += w;
+                acc.add(x[i][j], w);
+            }
+        }
+        const float peak = __shfl_sync(0xffffffffu, top, LANES * i);
+        if (cnt[i] > MOST) {  // a long request among short ones
+            const float *o = a.ws_o + (int64_t)(row0 + i) * a.max_splits * D;
+            const float *l = a.ws_lse + (int64_t)(row0 + i) * a.max_splits;
+            for (int j0 = MOST; j0 < cnt[i]; j0 += MOST) {
+                Acc<D> y[MOST];
+                float w[MOST];
+#pragma unroll
+                for (int j = 0; j < MOST; ++j)
+                    if (j0 + j < cnt[i]) {
+                        y[j].load(o + (j0 + j) * D, lane);
+                        w[j] = l[j0 + j];
+                    }
+#pragma unroll
+                for (int j = 0; j < MOST; ++j)
+                    if (j0 + j < cnt[i]) {
+                        const float e = __expf(w[j] - peak);
+                        sum += e;
+                        acc.add(y[j], e);
+                    }
+            }
+        }
+        if (cnt[i] != 1) acc.write(a.out, row0 + i, lane, cnt[i] == 0 ? 1.f : 1.f / sum);
+    }
+}
+
+// A few rows of many partials: a block of 8 warps takes one row, a warp every
+// 8th partial.
+template <int D>
+__global__ void __launch_bounds__(256) merge_row_kernel(const DecodeArgs a) {
+    constexpr int WARPS = 8, MOST = 8;
+    __shared__ float s_acc[WARPS][D], s_sum[WARPS];
+    const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+    const float *lse = a.ws_lse + (int64_t)row * a.max_splits, *o = a.ws_o + (int64_t)row * a.max_splits * D;
+    const float l0 = lane < a.max_splits ? lse[lane] : 0.f;
+    const int n = partials_of(a, row);
+    if (n == 1) return;
+    float top = lane < n ? l0 : -INFINITY;
+    for (int s = lane + 32; s < n; s += 32) top = fmaxf(top, lse[s]);
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    Acc<D> acc;
+    acc.clear();
+    float sum = 0.f;
+    for (int j0 = warp; j0 < n; j0 += WARPS * MOST) {
+        Acc<D> y[MOST];
+        float w[MOST];
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (j0 + j * WARPS < n) {
+                y[j].load(o + (j0 + j * WARPS) * D, lane);
+                w[j] = lse[j0 + j * WARPS];
+            }
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+            if (j0 + j * WARPS < n) {
+                const float e = __expf(w[j] - top);
+                sum += e;
+                acc.add(y[j], e);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < Acc<D>::CPL; ++i) s_acc[warp][lane * Acc<D>::CPL + i] = acc.c[i];
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    if (threadIdx.x < D / 2) {
+        float lo = 0.f, hi = 0.f, all = 0.f;
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            lo += s_acc[w][2 * threadIdx.x];
+            hi += s_acc[w][2 * threadIdx.x + 1];
+            all += s_sum[w];
+        }
+        const float scale = n == 0 ? 1.f : 1.f / all;
+        reinterpret_cast<uint32_t *>(a.out)[(int64_t)row * (D / 2) + threadIdx.x] = pack_bf16x2(lo * scale, hi * scale);
+    }
+}
+
 template <int D, int NG, int HEADS>
 cudaError_t launch_cfg(const DecodeFp8Args &args, cudaStream_t s) {
     const DecodeArgs &a = args.d;
     Layout lay;
-    lay.heads = fp4::block_heads(a.num_kv_heads);
-    lay.hblocks = (a.num_kv_heads + lay.heads - 1) / lay.heads;
+    lay.hblocks = (a.num_kv_heads + HEADS - 1) / HEADS;
     auto kern = decode_fp8_kernel<D, NG, HEADS>;
     int optin = 0;
     cudaError_t e = raise_limit(kern, optin);
@@ -268,22 +450,33 @@ cudaError_t launch_cfg(const DecodeFp8Args &args, cudaStream_t s) {
     e = launch_pdl(kern, dim3((unsigned)grid), dim3(HEADS * lay.subs * 32), smem, s, args,
                    a.sm_scale * split::LOG2E, lay);
     if (e != cudaSuccess || lay.whole) return e;
-    const int64_t rows = (int64_t)a.batch * a.num_q_heads;  // up to 4 CTAs of 4 an SM: the wide form
-    return launch_pdl(rows <= 16 * sms ? split::decode_merge_kernel<D, 16> : split::decode_merge_kernel<D, 4>,
-                      dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s, a);
+    const int64_t rows = (int64_t)a.batch * a.num_q_heads;
+    if (streams * MERGE_MANY < sms * lay.subs)
+        return launch_pdl(merge_row_kernel<D>, dim3((unsigned)rows), dim3(256), 0, s, a);
+    constexpr int per_cta = MERGE_THREADS / 32 * MERGE_ROWS;
+    return launch_pdl(merge_rows_kernel<D>, dim3((unsigned)((rows + per_cta - 1) / per_cta)), dim3(MERGE_THREADS), 0, s, a);
 }
 
 }  // namespace
 
 template <int D, int NG>
 cudaError_t launch_decode_fp8_as(const DecodeFp8Args &a, cudaStream_t s) {
-    switch (fp4::block_heads(a.d.num_kv_heads)) {
+    switch (fp8::block_heads<D>(a.d.num_kv_heads)) {
         case 1: return launch_cfg<D, NG, 1>(a, s);
         case 2: return launch_cfg<D, NG, 2>(a, s);
-        case 3:
+        case 3: return launch_cfg<D, NG, 3>(a, s);
         case 4: return launch_cfg<D, NG, 4>(a, s);
-        default: return launch_cfg<D, NG, 8>(a, s);
+        default: break;
     }
+    if constexpr (fp8::MOST_HEADS<D> > 4) {
+        switch (fp8::block_heads<D>(a.d.num_kv_heads)) {
+            case 5: return launch_cfg<D, NG, 5>(a, s);
+            case 6: return launch_cfg<D, NG, 6>(a, s);
+            case 7: return launch_cfg<D, NG, 7>(a, s);
+            default: return launch_cfg<D, NG, 8>(a, s);
+        }
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <int D, int NG>
