@@ -6,7 +6,11 @@
 // Bound by HBM: 16 bytes in and 32 out for 16 channels, so writes are two
 // thirds of it.  A thread keeps one column (K or V, and 16 channels) for all
 // its tokens; a block looks up the pool rows of a tile of tokens while it
-// converts the one before.
+// converts the one before.  328k tokens of 8 heads of 128: 329 us, 6.1 TB/s, 4.1
+// of them writes (a fill writes 3.8); 31k tokens 35.3 us (5.4).  More threads an SM
+// or fewer pieces in flight 342 to 460 and 35 to 50, streaming or evict-first
+// stores 334 and 341, tiles of 64 tokens 325, but 60 instead of 47 us for 41k
+// tokens in 40 requests.
 #include <algorithm>
 
 #include "fp8.cuh"

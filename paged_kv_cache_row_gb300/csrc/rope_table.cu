@@ -10,9 +10,11 @@
 // are their Taylor polynomials up to x^10 and x^9, whose first terms left out
 // are below 2^-32 and 2^-29.
 //
-// Bound by HBM writes, 4 rotary_dim bytes a position, if a pair takes few
+// Bound by writes, 4 rotary_dim bytes a position, if a pair takes few
 // instructions: a thread keeps four frequencies in registers and goes over
-// positions.
+// positions.  131072 positions of 128 channels: 14.1 us, 4.8 TB/s of writes (a
+// copy moves 6.8 TB/s, half of them reads; a fill of more than L2 writes 3.8).
+// With the frequencies read from the parameters by every thread 15.3.
 #include <algorithm>
 
 #include "kernels.h"
@@ -50,8 +52,7 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) rope_table_kernel(const __g
     const int h = a.rotary_dim / 2, per_row = h / 4;
     if ((int)threadIdx.x < h) s_turns[threadIdx.x] = a.turns[threadIdx.x];
     __syncthreads();
-    pdl_wait();
-    pdl_launch_dependents();
+    pdl_wait();  // no early start for the next kernel: rope_store_kv reads the table with non-coherent loads
     const int sub = threadIdx.x / per_row, j = (threadIdx.x - sub * per_row) * 4;
     if (sub >= rows) return;
     uint64_t f[4];
