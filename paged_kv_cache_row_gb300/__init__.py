@@ -989,8 +989,10 @@ def minisgl_rope_table(rope: Rope, positions: torch.Tensor, out: Optional[torch.
         _at(out, "out", torch.float32, dev)
         if out.shape != (n, width) or not out.is_contiguous():
             raise MinisglError("out must be contiguous [n, rotary_dim] float32")
-    _check(load_library().minisgl_rope_table(rope._turns, rope.attention_factor, width, positions.data_ptr(), n,
-                                             out.data_ptr(), _raw_stream(dev)), "rope_table")
+    rc = (_lib or load_library()).minisgl_rope_table(rope._turns, rope.attention_factor, width, positions.data_ptr(),
+                                                     n, out.data_ptr(), _raw_stream(dev))
+    if rc:
+        _check(rc, "rope_table")
     return out
 
 
@@ -1058,10 +1060,6 @@ class KVPoolFP8:
         return cls(torch.zeros((2, num_layers, num_rows, num_kv_heads, head_dim), dtype=torch.uint8, device=device),
                    scales[..., :num_kv_heads], page_size, block_tokens)
 
-    def _desc(self, layer: int):
-        if not 0 <= layer < self.num_layers:
-            raise MinisglError(f"layer {layer} outside [0, {self.num_layers})")
-        return self._ref
 
 
 def kv_pool_fp8_bytes(num_layers: int, num_kv_heads: int, head_dim: int, num_tokens: int,
@@ -1083,8 +1081,10 @@ def minisgl_store_kv_fp8(pool: KVPoolFP8, layer: int, k: torch.Tensor, v: torch.
     n = out_loc.numel()
     _vec(out_loc, "out_loc", None, dev)
     ks, vs = _kv_rows(k, "k", n, row, dev), _kv_rows(v, "v", n, row, dev)
-    _check(load_library().minisgl_store_kv_fp8(pool._desc(layer), layer, k.data_ptr(), v.data_ptr(), ks, vs,
-                                               out_loc.data_ptr(), n, _raw_stream(dev)), "store_kv_fp8")
+    rc = (_lib or load_library()).minisgl_store_kv_fp8(pool._ref, layer, k.data_ptr(), v.data_ptr(), ks, vs,
+                                                       out_loc.data_ptr(), n, _raw_stream(dev))
+    if rc:
+        _check(rc, "store_kv_fp8")
 
 
 def minisgl_rope_store_kv_fp8(pool: KVPoolFP8, layer: int, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -1119,10 +1119,12 @@ def minisgl_rope_store_kv_fp8(pool: KVPoolFP8, layer: int, q: torch.Tensor, k: t
     if cos_sin_cache.dim() != 2 or not cos_sin_cache.is_contiguous():
         raise MinisglError("cos_sin_cache must be contiguous [max_positions, rotary_dim] float32")
     most, rotary = cos_sin_cache.shape
-    _check(load_library().minisgl_rope_store_kv_fp8(
-        pool._desc(layer), layer, q.data_ptr(), shape[1], qs, q_out.data_ptr(), outs, k.data_ptr(), v.data_ptr(), ks,
+    rc = (_lib or load_library()).minisgl_rope_store_kv_fp8(
+        pool._ref, layer, q.data_ptr(), shape[1], qs, q_out.data_ptr(), outs, k.data_ptr(), v.data_ptr(), ks,
         vs, positions.data_ptr(), cos_sin_cache.data_ptr(), most, rotary, 1 if interleaved else 0, out_loc.data_ptr(),
-        n, _raw_stream(dev)), "rope_store_kv_fp8")
+        n, _raw_stream(dev))
+    if rc:
+        _check(rc, "rope_store_kv_fp8")
     return q_out
 
 
@@ -1149,9 +1151,11 @@ def minisgl_load_kv_fp8(pool: KVPoolFP8, layer: int, page_table: torch.Tensor, l
         k_out = _new((total, H, d), (row, d, 1), _BF16)
     if v_out is None:
         v_out = _new((total, H, d), (row, d, 1), _BF16)
-    _check(load_library().minisgl_load_kv_fp8(pool._desc(layer), layer, page_table.data_ptr(), B, stride, width,
-                                              lens.data_ptr(), offsets.data_ptr(), total, k_out.data_ptr(),
-                                              v_out.data_ptr(), ks, vs, _raw_stream(dev)), "load_kv_fp8")
+    rc = (_lib or load_library()).minisgl_load_kv_fp8(
+        pool._ref, layer, page_table.data_ptr(), B, stride, width, lens.data_ptr(), offsets.data_ptr(), total,
+        k_out.data_ptr(), v_out.data_ptr(), ks, vs, _raw_stream(dev))
+    if rc:
+        _check(rc, "load_kv_fp8")
     return k_out, v_out
 
 
@@ -1194,8 +1198,10 @@ def minisgl_decode_attn_fp8(pool: KVPoolFP8, layer: int, q: torch.Tensor, page_t
         workspace = decode_workspace_fp8(B, Hq, pool, max_splits)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise MinisglError("workspace must be a contiguous CUDA tensor on the pool's device")
-    _check(load_library().minisgl_decode_attn_fp8(
-        pool._desc(layer), layer, q.data_ptr(), Hq, page_table.data_ptr(), B, stride, width, seq_lens.data_ptr(),
+    rc = (_lib or load_library()).minisgl_decode_attn_fp8(
+        pool._ref, layer, q.data_ptr(), Hq, page_table.data_ptr(), B, stride, width, seq_lens.data_ptr(),
         float(sm_scale), out.data_ptr(), workspace.data_ptr(), workspace.nbytes, split_tokens,
-        _raw_stream(dev)), "decode_attn_fp8")
+        _raw_stream(dev))
+    if rc:
+        _check(rc, "decode_attn_fp8")
     return out
