@@ -34,6 +34,7 @@
 // 176 (groups of warps, q by four heads a token) - 166 (fetched a run ahead) -
 // 151 (windows of a block's rows, where windows of 32 tokens left half the groups
 // with twice the work; the next head of the same run instead of the next run).
+// The rotation in packed pairs of fp32 took 157, and 44 instead of 41 on the third.
 #include <algorithm>
 
 #include "fp8.cuh"
