@@ -5,12 +5,12 @@
 //
 // Bound by HBM: 16 bytes in and 32 out for 16 channels, so writes are two
 // thirds of it.  A thread keeps one column (K or V, and 16 channels) for all
-// its tokens; a block looks up the pool rows of a tile of tokens while it
-// converts the one before.  328k tokens of 8 heads of 128: 329 us, 6.1 TB/s, 4.1
-// of them writes (a fill writes 3.8); 31k tokens 35.3 us (5.4).  More threads an SM
-// or fewer pieces in flight 342 to 460 and 35 to 50, streaming or evict-first
-// stores 334 and 341, tiles of 64 tokens 325, but 60 instead of 47 us for 41k
-// tokens in 40 requests.
+// its tokens and asks for its next pieces before it converts those it has; a
+// block looks up the pool rows of a tile of tokens while it converts the one
+// before.  328k tokens of 8 heads of 128: 326 us, 6.2 TB/s (a copy of as many bytes
+// runs at 6.9); 31k tokens 33.4 us (5.6).  With a run of tiles to each block 328 and
+// 35.2, without asking ahead 331 and 35.4; half the threads with 8 pieces in
+// flight 322 and 34.4, but 60 instead of 44 us for 41k tokens in 40 requests.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -24,7 +24,7 @@ namespace {
 constexpr int MAX_THREADS = 512;
 constexpr int RESIDENT = 1024;   // threads per SM
 constexpr int IN_FLIGHT = 4;     // pieces of 16 channels that a thread has under way
-constexpr int TILE_TOKENS = 128; // most tokens of a tile
+constexpr int MOST_TOKENS = 128; // of a tile
 
 __device__ __forceinline__ uint4 ld_v4(const void *p) {  // coherent, as in the store
     uint4 v;
@@ -49,46 +49,39 @@ __device__ __forceinline__ void st_32(void *p, const uint32_t (&x)[8]) {
 
 }  // namespace
 
-// A block takes a run of tiles of tile_toks tokens, one thread per column of
-// `toks` tokens at a time (with more columns than threads it goes over them in
-// steps).  The request of a run's first tokens is found by binary search, the
-// later ones by walking on.
+// A block takes every gridDim.x-th tile of tile_toks tokens (so that the blocks
+// together write one place at a time), one thread per column of `toks` tokens at a
+// time (with more columns than threads it goes over them in steps).
 template <bool WIDE>
 __global__ void __launch_bounds__(MAX_THREADS, RESIDENT / MAX_THREADS)
     load_kv_fp8_kernel(const LoadFp8Args a, int pieces, int toks, int tile_toks) {
-    __shared__ int s_row[2][TILE_TOKENS];  // pool row of each token, or -1
+    __shared__ int s_row[2][MOST_TOKENS];  // pool row of each token, or -1
     pdl_wait();  // no early start for the next kernel: store_kv may read the rows with non-coherent loads
     const int64_t tiles = ((int64_t)a.total_tokens + tile_toks - 1) / tile_toks;
-    const int64_t first = blockIdx.x * tiles / gridDim.x, last = (blockIdx.x + 1) * tiles / gridDim.x;
-    int req = -1;  // lane's request
     auto look_up = [&](int64_t tile, int *rows) {
         const int64_t t = tile * tile_toks + threadIdx.x;
         int row = -1;
         if (t < a.total_tokens) {
-            if (req < 0) {
-                int lo = 0, hi = a.batch;  // the last request with offsets[r] <= t
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (a.offsets[mid] <= t) lo = mid; else hi = mid;
-                }
-                req = lo;
+            int req = 0, hi = a.batch;  // the last request with offsets[r] <= t
+            while (hi - req > 1) {
+                const int mid = (req + hi) >> 1;
+                if (a.offsets[mid] <= t) req = mid; else hi = mid;
             }
-            int end = a.offsets[req + 1];
-            while (req + 1 < a.batch && end <= t) end = a.offsets[++req + 1];
             const int64_t j = t - a.offsets[req];
             const int n = min(max(a.lens[req], 0), a.pt_width);
-            if (j >= 0 && j < n && t < end)
+            if (j >= 0 && j < n && t < a.offsets[req + 1])
                 row = min(max(a.page_table[req * a.pt_stride + j], 0), a.pool.num_rows - 1);
         }
         rows[threadIdx.x] = row;
     };
     const int per_head = a.pool.head_dim / 16;
     const int sub = threadIdx.x / (2 * pieces);
-    if ((int)threadIdx.x < tile_toks && first < last) look_up(first, s_row[0]);
-    for (int64_t tile = first; tile < last; ++tile) {
-        const int *rows = s_row[(tile - first) & 1];
+    if ((int)threadIdx.x < tile_toks && blockIdx.x < tiles) look_up(blockIdx.x, s_row[0]);
+    int at = 0;
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, at ^= 1) {
+        const int *rows = s_row[at];
         __syncthreads();
-        if ((int)threadIdx.x < tile_toks && tile + 1 < last) look_up(tile + 1, s_row[(tile + 1 - first) & 1]);
+        if ((int)threadIdx.x < tile_toks && tile + gridDim.x < tiles) look_up(tile + gridDim.x, s_row[at ^ 1]);
         if (sub >= toks) continue;
         for (int col = threadIdx.x - sub * 2 * pieces; col < 2 * pieces; col += blockDim.x) {
             const bool is_v = col >= pieces;
@@ -98,23 +91,32 @@ __global__ void __launch_bounds__(MAX_THREADS, RESIDENT / MAX_THREADS)
             const int64_t tok_stride = is_v ? a.v_tok_stride : a.k_tok_stride;
             __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(is_v ? a.v_out : a.k_out) +
                                  tile * tile_toks * tok_stride + piece * 16;
-            for (int i0 = sub; i0 < tile_toks; i0 += IN_FLIGHT * toks) {
-                uint4 c[IN_FLIGHT];
-                uint32_t e[IN_FLIGHT];
-                int row[IN_FLIGHT];
+            // the next pieces are asked for before these are converted and stored
+            uint4 c[IN_FLIGHT], next[IN_FLIGHT];
+            uint32_t e[IN_FLIGHT], next_e[IN_FLIGHT];
+            auto ask = [&](int i0, uint4 (&x)[IN_FLIGHT], uint32_t (&scale_of)[IN_FLIGHT]) {
 #pragma unroll
                 for (int u = 0; u < IN_FLIGHT; ++u) {
-                    const int i = i0 + u * toks;
-                    row[u] = i < tile_toks ? rows[i] : -1;
-                    if (row[u] >= 0) {
-                        const uint32_t r = (uint32_t)row[u];
-                        c[u] = ld_v4(data + (uint64_t)r * (uint32_t)a.pool.data_stride);
-                        e[u] = scale[(uint64_t)(r >> a.pool.block_log2) * (uint32_t)a.pool.scale_stride];
+                    const int i = i0 + u * toks, row = i < tile_toks ? rows[i] : -1;
+                    scale_of[u] = ~0u;  // none
+                    if (row >= 0) {
+                        const uint32_t r = (uint32_t)row;
+                        x[u] = ld_v4(data + (uint64_t)r * (uint32_t)a.pool.data_stride);
+                        scale_of[u] = scale[(uint64_t)(r >> a.pool.block_log2) * (uint32_t)a.pool.scale_stride];
                     }
                 }
+            };
+            ask(sub, next, next_e);
+            for (int i0 = sub; i0 < tile_toks; i0 += IN_FLIGHT * toks) {
 #pragma unroll
                 for (int u = 0; u < IN_FLIGHT; ++u) {
-                    if (row[u] < 0) continue;
+                    c[u] = next[u];
+                    e[u] = next_e[u];
+                }
+                if (i0 + IN_FLIGHT * toks < tile_toks) ask(i0 + IN_FLIGHT * toks, next, next_e);
+#pragma unroll
+                for (int u = 0; u < IN_FLIGHT; ++u) {
+                    if (e[u] == ~0u) continue;
                     const float unit = __uint_as_float(e[u] << 23);
                     const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
                     uint32_t o[8];
@@ -138,9 +140,11 @@ cudaError_t launch_load_kv_fp8(const LoadFp8Args &a, cudaStream_t s) {
     const int pieces = a.pool.num_kv_heads * a.pool.head_dim / 16, columns = 2 * pieces;
     const int toks = columns < 256 ? 256 / columns : 1;
     const int threads = (int)std::min<int64_t>(((int64_t)toks * columns + 31) / 32 * 32, MAX_THREADS);
-    // tiles as large as still give every resident block one; at least a step of the block
+    // Tiles of 32 tokens, or of a block's step with all pieces in flight; smaller ones
+    // if that leaves resident blocks without one, but at least a step of the block.
     const int64_t cap = (int64_t)device_sm_count() * (RESIDENT / threads);
-    const int tile = (int)std::min<int64_t>(TILE_TOKENS, std::max<int64_t>(toks, (a.total_tokens + cap - 1) / cap));
+    const int most = std::max(32, toks * IN_FLIGHT);  // up to MOST_TOKENS: toks is up to 32
+    const int tile = (int)std::min<int64_t>(most, std::max<int64_t>(toks, (a.total_tokens + cap - 1) / cap));
     const int64_t blocks = std::min(cap, ((int64_t)a.total_tokens + tile - 1) / tile);
     auto wide = [](const void *p, int64_t tok_stride) {
         return (reinterpret_cast<uintptr_t>(p) & 31u) == 0 && tok_stride % 16 == 0;
