@@ -34,7 +34,9 @@
 // 176 (groups of warps, q by four heads a token) - 166 (fetched a run ahead) -
 // 151 (windows of a block's rows, where windows of 32 tokens left half the groups
 // with twice the work; the next head of the same run instead of the next run).
-// The rotation in packed pairs of fp32 took 157, and 44 instead of 41 on the third.
+// The rotation in packed pairs of fp32 took 157, and 44 instead of 41 on the third;
+// cos and sin kept for all heads of a run and K rotated twice instead (for the
+// maximum and again) 146, but 38 instead of 36.4 on the second, with spills.
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -323,27 +325,45 @@ struct Runs {
     }
 };
 
-// A group's share of the work on K (or V): W warps, C rows to a lane; row l of a
-// run is a lane's if l = g + c * W * RPW.
-template <int D, int W, int C, bool IS_K>
+// K or V: the new rows and where they go.
+struct Side {
+    const __nv_bfloat16 *src;  // token 0
+    int64_t tok_stride;
+    uint8_t *data, *scale;     // row 0, block 0
+};
+__device__ __forceinline__ Side side_of(const StoreFp8Args &a, bool is_k) {
+    Side x;
+    x.src = static_cast<const __nv_bfloat16 *>(is_k ? a.k : a.v);
+    x.tok_stride = is_k ? a.k_tok_stride : a.v_tok_stride;
+    x.data = is_k ? a.pool.k_data : a.pool.v_data;
+    x.scale = is_k ? a.pool.k_scale : a.pool.v_scale;
+    return x;
+}
+
+// A group's share of the work on K or V: W warps, C rows to a lane; row l of a
+// run is a lane's if l = g + c * W * RPW.  TURN: the rows are rotated (K), and
+// stay in registers in fp32 until the maximum is known; else they stay in shared
+// memory, and the maximum and the scaling (exact in bf16) take two at a time.
+template <int D, int W, int C, bool TURN>
 struct Group {
     static constexpr int TPR = D / 16, RPW = 32 / TPR;  // lanes per row, rows per warp
     int lane, part, group, t, g;
     Chunks ch;
+    Side side;
 
-    __device__ __forceinline__ Group(const StoreFp8Args &a) {
+    __device__ __forceinline__ Group(const StoreFp8Args &a, bool is_k) {
+        side = side_of(a, is_k);
         lane = threadIdx.x & 31;
         const int warp = threadIdx.x >> 5;
         part = warp % W;
         group = warp / W;
         t = lane % TPR;
         g = part * RPW + lane / TPR;
-        ch = chunks_of<D>(t, IS_K ? a.rotary_dim : 0);
+        ch = chunks_of<D>(t, TURN ? a.rotary_dim : 0);
     }
 
     __device__ __forceinline__ uint8_t *scale_of(const StoreFp8Args &a, const Run &run) const {
-        return (IS_K ? a.pool.k_scale : a.pool.v_scale) + run.head +
-               (run.row0 >> a.pool.block_log2) * a.pool.scale_stride;
+        return side.scale + run.head + (run.row0 >> a.pool.block_log2) * a.pool.scale_stride;
     }
 
     // The lane's rows of a head on their way to its place in shared memory, and the
@@ -351,16 +371,15 @@ struct Group {
     __device__ __forceinline__ void fetch(const StoreFp8Args &a, const Run &run, uint32_t to, bool first,
                                           int (&position)[C], int &before) const {
         before = run.off > 0 ? (int)*scale_of(a, run) : fp8::EXP_BIAS + fp8::EXP_LOW;
-        const int64_t stride = IS_K ? a.k_tok_stride : a.v_tok_stride;
-        const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(IS_K ? a.k : a.v) + run.head * D + run.i0 * stride;
+        const __nv_bfloat16 *src = side.src + run.head * D + run.i0 * side.tok_stride;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int l = g + c * W * RPW;
             const bool live = l < run.len;
-            const __nv_bfloat16 *row = src + (live ? l : 0) * stride;
+            const __nv_bfloat16 *row = src + (live ? l : 0) * side.tok_stride;
             cp_async_16(to + (2 * c) * THREADS * 16, row + ch.a, live ? 16 : 0);
             cp_async_16(to + (2 * c + 1) * THREADS * 16, row + ch.b, live ? 16 : 0);
-            if (IS_K && first) position[c] = ch.turned && live ? a.positions[run.i0 + l] : 0;
+            if (TURN && first) position[c] = ch.turned && live ? a.positions[run.i0 + l] : 0;
         }
     }
 
@@ -387,10 +406,10 @@ struct Group {
 
     __device__ __forceinline__ void store(const StoreFp8Args &a, const Run &run, uint32_t from, const int (&position)[C],
                                           int before, uint32_t (&s_top)[2][W], int &round) const {
-        uint8_t *data = (IS_K ? a.pool.k_data : a.pool.v_data) + run.head * D + run.row0 * a.pool.data_stride;
-        float x[IS_K ? C : 1][16];
+        uint8_t *data = side.data + run.head * D + run.row0 * a.pool.data_stride;
+        float x[TURN ? C : 1][16];
         uint32_t top = 0;
-        if constexpr (IS_K) {
+        if constexpr (TURN) {
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 uint32_t va[4], vb[4];
@@ -420,8 +439,8 @@ struct Group {
             top = 0;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                float (&y)[16] = x[IS_K ? c : 0];
-                if constexpr (!IS_K) {
+                float (&y)[16] = x[TURN ? c : 0];
+                if constexpr (!TURN) {
                     uint32_t va[4], vb[4];
                     words(from, c, va, vb);
                     widen(make_uint4(va[0], va[1], va[2], va[3]), make_uint4(vb[0], vb[1], vb[2], vb[3]), y);
@@ -455,7 +474,7 @@ struct Group {
         for (int c = 0; c < C; ++c) {
             const int l = g + c * W * RPW;
             if (l >= run.len) continue;
-            if constexpr (IS_K) {
+            if constexpr (TURN) {
                 put(data + l * a.pool.data_stride, ch, x[c], pow2i(-e));
             } else {  // an exact product in bf16: what it loses to underflow is far below half an element
                 uint32_t v[8];
@@ -471,13 +490,13 @@ struct Group {
     }
 };
 
-// K's (or V's) units from u on; a group fetches its next head of a run, or its
+// K's or V's units from u on; a group fetches its next head of a run, or its
 // next run, while it works on one.  place: the thread's in shared memory.
-template <int D, int W, int C, bool IS_K>
-__device__ __forceinline__ void store_all(const StoreFp8Args &a, uint32_t &u, uint32_t step, int win_log2, int heads,
+template <int D, int W, int C, bool TURN>
+__device__ __forceinline__ void store_all(const StoreFp8Args &a, bool is_k, uint32_t &u, uint32_t step, int win_log2, int heads,
                                           uint32_t place, uint32_t (&s_top)[2][W], int &round) {
     constexpr uint32_t PLACE = 2 * C * THREADS * 16;
-    const Group<D, W, C, IS_K> w(a);
+    const Group<D, W, C, TURN> w(a, is_k);
     Runs runs;
     runs.init(a, win_log2, heads, u, step, w.lane);
     Run run, next;
@@ -497,7 +516,7 @@ __device__ __forceinline__ void store_all(const StoreFp8Args &a, uint32_t &u, ui
         w.store(a, run, place + at, position, before, s_top, round);
         run = next;
         before = before_ahead;
-        if (IS_K && fresh) {
+        if (TURN && fresh) {
 #pragma unroll
             for (int c = 0; c < C; ++c) position[c] = ahead[c];
         }
@@ -508,8 +527,8 @@ __device__ __forceinline__ void store_all(const StoreFp8Args &a, uint32_t &u, ui
 
 }  // namespace
 
-// Blocks of W * C * 512 / d rows.  K's units, then V's, then q's.
-template <int D, int W, int C>
+// Blocks of W * C * 512 / d rows.  K's units (TURN: rotated), then V's, then q's.
+template <int D, int W, int C, bool TURN>
 __global__ void __launch_bounds__(THREADS, RESIDENT) store_kv_fp8_kernel(const StoreFp8Args a, int win_log2, int heads) {
     // two places for a lane's rows: [place][chunk of a row][thread], 16 bytes each
     __shared__ __align__(16) uint8_t s_rows[2][2 * C][THREADS][16];
@@ -520,8 +539,11 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) store_kv_fp8_kernel(const S
     const uint32_t step = gridDim.x * (WARPS / W), place = smem_u32(&s_rows[0][0][threadIdx.x][0]);
     uint32_t u = blockIdx.x * (WARPS / W) + group;
     int round = 0;
-    store_all<D, W, C, true>(a, u, step, win_log2, heads, place, s_top[group], round);
-    store_all<D, W, C, false>(a, u, step, win_log2, heads, place, s_top[group], round);
+    if constexpr (TURN) store_all<D, W, C, true>(a, true, u, step, win_log2, heads, place, s_top[group], round);
+#pragma unroll 1
+    for (int is_k = TURN ? 0 : 1; is_k >= 0; --is_k)
+        store_all<D, W, C, false>(a, is_k, u, step, win_log2, heads, place, s_top[group], round);
+    if constexpr (!TURN) return;
     // q: one unit of by_token for each warp, the groups' numbers going on
     const uint32_t chunks = head_chunks(a.num_q_heads), last = (a.n_tokens + 512 / D - 1) / (512 / D) * chunks;
     for (uint32_t v = u * W + warp % W; v < last; v += step * W) by_token<D, QUERY>(a, v, chunks, threadIdx.x & 31);
@@ -560,7 +582,8 @@ cudaError_t launch_runs(const StoreFp8Args &a, cudaStream_t s) {
     const int64_t q_units = (n + 512 / D - 1) / (512 / D) * head_chunks(a.num_q_heads);
     const int64_t blocks =
         std::min((units(win, (H + heads - 1) / heads) + (q_units + W - 1) / W + groups - 1) / groups, resident);
-    return launch_pdl(store_kv_fp8_kernel<D, W, C>, dim3((unsigned)blocks), dim3(THREADS), 0, s, a, win, (int)heads);
+    return launch_pdl(a.rotary_dim ? store_kv_fp8_kernel<D, W, C, true> : store_kv_fp8_kernel<D, W, C, false>,
+                      dim3((unsigned)blocks), dim3(THREADS), 0, s, a, win, (int)heads);
 }
 
 template <int D>
