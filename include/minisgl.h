@@ -63,7 +63,8 @@
  *     minisgl_extend_attn (with minisgl_store_kv; with and without a caller
  *     work counter), minisgl_cascade_decode_attn (including its fork onto the
  *     library's second stream and the join back) and
- *     minisgl_cascade_extend_attn are tested captured in a CUDA graph and
+ *     minisgl_cascade_extend_attn, and the calls of the 4-bit and 8-bit pools,
+ *     are tested captured in a CUDA graph and
  *     replayed, with their pointers fixed; the first cascade-decode call on a
  *     device creates that stream and its events, so make it before capture.
  *   - Return value: MINISGL_OK, or a negative MINISGL_ERR_* code with a
