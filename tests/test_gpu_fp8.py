@@ -756,6 +756,92 @@ def test_rows_past_32_bit_offsets():
     assert torch.equal(a, check_decode(small, q[:1].contiguous(), near, [n], 0.1))
 
 
+def off_by_16_bytes(shape, seed=None):
+    """A bf16 tensor of this shape whose first element is 16 bytes past a 256-byte border."""
+    n = int(np.prod(shape))
+    t = torch.full((n + 8,), 9.0, dtype=torch.bfloat16, device=DEV)[8:].view(shape)
+    if seed is not None:
+        t.copy_(kv_like(shape, seed))
+    assert t.data_ptr() % 32 == 16
+    return t
+
+
+@pytest.mark.parametrize("block", [1, 16, 64])
+@pytest.mark.parametrize("H,d", [(3, 64), (2, 128)])
+def test_everything_aligned_to_16_bytes_only(H, d, block):
+    """Rows of the pool 16 bytes longer than they need be, scales 4 bytes past a
+    border, and every tensor 16 bytes past one."""
+    R, n, Hq = 192, 100, 2 * H
+    raw = torch.full((2 * R * (H * d + 16) + 16,), 0x55, dtype=torch.uint8, device=DEV)[16:]
+    data = raw.as_strided((2, 1, R, H, d), (R * (H * d + 16), 0, H * d + 16, d, 1))
+    nb = R // block
+    sraw = torch.full((2 * nb * 12 + 16,), 100, dtype=torch.uint8, device=DEV)[4:]
+    scales = sraw.as_strided((2, 1, nb, H), (nb * 12, 0, 12, 1))
+    pool = mk.KVPoolFP8(data, scales, 64, block)
+    q, k, v = (off_by_16_bytes((n, h, d), h + i) for i, h in enumerate((Hq, H, H)))
+    rows = list(range(40, 40 + n))
+    cache = mk.minisgl_rope_table(mk.Rope(d), i32(range(500)))
+    pos = np.arange(n) * 3
+    (before, (vc, ve)) = pool_state(pool)
+    kept = f64(q)
+    out = mk.minisgl_rope_store_kv_fp8(pool, 0, q, k, v, i32(pos), cache, i32(rows), interleaved=True,
+                                       q_out=off_by_16_bytes((n, Hq, d)))
+    want, off = ref.rotate(kept, f64(cache)[pos], True)
+    assert (np.abs(f64(out) - want) <= 2.0 ** -8 * np.abs(want) + 2 * off).all()
+    check_rotated_store(pool, before, rows, *ref.rotate(f64(k), f64(cache)[pos], True))
+    ref.store(vc, ve, rows, f64(v), block)
+    got = pool_state(pool)[1]
+    assert np.array_equal(got[0], vc) and np.array_equal(got[1], ve)
+    assert (raw.as_strided((2, R, 16), (R * (H * d + 16), H * d + 16, 1), raw.storage_offset() + H * d) == 0x55).all()
+    store_and_check(pool, rows, k.cpu(), v.cpu(), 0, k, v)
+    ko, vo = off_by_16_bytes((n + 1, H, d)), off_by_16_bytes((n + 1, H, d))
+    mk.minisgl_load_kv_fp8(pool, 0, i32([rows]), i32([n]), i32([0, n]), n + 1, ko, vo)
+    for got, vals in zip((ko, vo), pool_values(pool)):
+        assert np.array_equal(f64(got[:n]), vals[rows]) and (got[n] == 9).all()
+    table = i32(np.random.default_rng(0).integers(40, 40 + n, (3, 133)))
+    qd = off_by_16_bytes((3, Hq, d), 5)
+    check_decode(pool, qd, table, [133, 1, 64], 0.1, out=off_by_16_bytes((3, Hq, d)))
+
+
+@pytest.mark.parametrize("B,Hq,H,d,long", [(160, 8, 4, 128, 20000), (320, 6, 2, 64, 9000), (90, 16, 8, 128, 5000)])
+def test_decode_a_long_request_among_many(B, Hq, H, d, long):
+    """More partials of one request than a warp has under way in the merge of many rows."""
+    lens = np.random.default_rng(B).integers(0, 40, B)
+    lens[B // 3] = long
+    pool, q, table = case(B, Hq, H, d, 16, lens, B)
+    check_decode(pool, q, table, lens, d ** -0.5)
+    check_decode(pool, q, table, lens, d ** -0.5, max_splits=200)
+
+
+@pytest.mark.parametrize("width", [1, 31, 33, 65, 1000])
+def test_decode_table_widths(width):
+    lens = [width, 1, 0, max(1, width // 2)]
+    pool, q, table = case(4, 8, 4, 64, 32, lens, width, width=width)
+    check_decode(pool, q, table, lens, 0.125)
+
+
+def test_calls_without_requests():
+    pool = new_pool(32, 2, 64, 16)
+    none, q = i32([]), torch.empty((0, 4, 64), dtype=torch.bfloat16, device=DEV)
+    assert mk.minisgl_decode_attn_fp8(pool, 0, q, torch.zeros((0, 32), dtype=torch.int32, device=DEV), none, 0.1).shape == (0, 4, 64)
+    k, v = mk.minisgl_load_kv_fp8(pool, 0, torch.zeros((0, 32), dtype=torch.int32, device=DEV), none, i32([0]), 0)
+    assert k.shape == v.shape == (0, 2, 64)
+    k = torch.full((3, 2, 64), 5.0, dtype=torch.bfloat16, device=DEV)
+    mk.minisgl_load_kv_fp8(pool, 0, i32([[1, 2]]), i32([0]), i32([0, 0]), 3, k, k.clone())
+    assert (k == 5).all()
+
+
+def test_store_without_queries():
+    """num_q_heads 0: K and V alone, rotated."""
+    pool, twin = new_pool(32, 2, 64, 16), new_pool(32, 2, 64, 16)
+    k, v, q = (kv_like((20, h, 64), h).to(DEV) for h in (2, 3, 4))
+    v = v[:, :2].contiguous()
+    cache, rows = mk.minisgl_rope_table(mk.Rope(32), i32(range(50))), i32(range(5, 25))
+    mk.minisgl_rope_store_kv_fp8(pool, 0, q[:, :0].contiguous(), k, v, rows, cache, rows)
+    mk.minisgl_rope_store_kv_fp8(twin, 0, q, k, v, rows, cache, rows)
+    check_state(pool, pool_state(twin))
+
+
 # --------------------------------------------------------------------------- #
 # streams, graphs, refusals
 # --------------------------------------------------------------------------- #
