@@ -27,16 +27,18 @@
 // known, which leaves 16 warps an SM.
 //
 // Measured (device time, in a graph): 133k tokens, 15 query and 5 KV heads of 64,
-// blocks of 64, half of the head rotated, 151 us (5.2 TB/s; q alone 6.3, K and V
-// without a rotation 5.4); 8.2k tokens, 32 and 8 heads of 128, blocks of 16, 36.4
-// us (5.3 TB/s); K and V of 41k tokens, 8 heads of 128, blocks of one row, 41 us (6.2
-// TB/s).  Steps on the first: 189 (a warp per run, read twice for the maximum) -
-// 176 (groups of warps, q by four heads a token) - 166 (fetched a run ahead) -
-// 151 (windows of a block's rows, where windows of 32 tokens left half the groups
-// with twice the work; the next head of the same run instead of the next run).
-// The rotation in packed pairs of fp32 took 157, and 44 instead of 41 on the third;
-// cos and sin kept for all heads of a run and K rotated twice instead (for the
-// maximum and again) 146, but 38 instead of 36.4 on the second, with spills.
+// blocks of 64, half of the head rotated, 147 us (5.3 TB/s; K and V without a
+// rotation 46, 5.5 TB/s, rotated 69); 8.2k tokens, 32 and 8 heads of 128, blocks of
+// 16, 34.1 us (5.6 TB/s); K and V of 41k tokens, 8 heads of 128, blocks of one row,
+// 41 us (6.2 TB/s).  Steps on the first: 189 (a warp per run, read twice for the
+// maximum) - 176 (groups of warps, q by four heads a token) - 166 (fetched a run
+// ahead) - 151 (windows of a block's rows, where windows of 32 tokens left half the
+// groups with twice the work; the next head of the same run instead of the next
+// run) - 147 (half of the blocks begin with q).  Not kept: the rotation in packed
+// pairs of fp32 (157, and 44 instead of 41 on the third); the table's rows asked
+// for ahead (152); cos and sin kept for all heads of a run and K rotated twice
+// instead, for the maximum and again (146 where 151 were taken, but 38 instead of
+// 36.4 on the second).
 #include <algorithm>
 
 #include "fp8.cuh"
@@ -527,9 +529,10 @@ __device__ __forceinline__ void store_all(const StoreFp8Args &a, bool is_k, uint
 
 }  // namespace
 
-// Blocks of W * C * 512 / d rows.  K's units (TURN: rotated), then V's, then q's.
+// Blocks of W * C * 512 / d rows.  K's units (TURN: rotated) and V's, and q's.
 template <int D, int W, int C, bool TURN>
-__global__ void __launch_bounds__(THREADS, RESIDENT) store_kv_fp8_kernel(const StoreFp8Args a, int win_log2, int heads) {
+__global__ void __launch_bounds__(THREADS, RESIDENT) store_kv_fp8_kernel(const StoreFp8Args a, int win_log2, int heads,
+                                                                          bool mixed) {
     // two places for a lane's rows: [place][chunk of a row][thread], 16 bytes each
     __shared__ __align__(16) uint8_t s_rows[2][2 * C][THREADS][16];
     __shared__ uint32_t s_top[WARPS / W][2][W];
@@ -539,14 +542,24 @@ __global__ void __launch_bounds__(THREADS, RESIDENT) store_kv_fp8_kernel(const S
     const uint32_t step = gridDim.x * (WARPS / W), place = smem_u32(&s_rows[0][0][threadIdx.x][0]);
     uint32_t u = blockIdx.x * (WARPS / W) + group;
     int round = 0;
+    // q: one unit of by_token for each warp, the groups' numbers going on behind K's and V's units
+    const uint32_t chunks = head_chunks(a.num_q_heads), last = (a.n_tokens + 512 / D - 1) / (512 / D) * chunks;
+    auto queries = [&](uint32_t first) {
+        for (uint32_t v = first * W + warp % W; v < last; v += step * W)
+            by_token<D, QUERY>(a, v, chunks, threadIdx.x & 31);
+    };
+    // In a full grid half of an SM's blocks begin with q, whose rows are bound by HBM,
+    // while the others have K, which is bound by more
+    const bool q_first = TURN && mixed && (blockIdx.x * RESIDENT / gridDim.x) % 2;
+    if (q_first) {
+        const uint32_t kv = 2u * ((a.n_tokens + (1 << win_log2) - 1) >> win_log2) * ((a.pool.num_kv_heads + heads - 1) / heads);
+        queries((u + step - kv % step) % step);
+    }
     if constexpr (TURN) store_all<D, W, C, true>(a, true, u, step, win_log2, heads, place, s_top[group], round);
 #pragma unroll 1
     for (int is_k = TURN ? 0 : 1; is_k >= 0; --is_k)
         store_all<D, W, C, false>(a, is_k, u, step, win_log2, heads, place, s_top[group], round);
-    if constexpr (!TURN) return;
-    // q: one unit of by_token for each warp, the groups' numbers going on
-    const uint32_t chunks = head_chunks(a.num_q_heads), last = (a.n_tokens + 512 / D - 1) / (512 / D) * chunks;
-    for (uint32_t v = u * W + warp % W; v < last; v += step * W) by_token<D, QUERY>(a, v, chunks, threadIdx.x & 31);
+    if (TURN && !q_first) queries(u);
 }
 
 // Blocks of one row: K's units, then V's, then q's.
@@ -583,7 +596,7 @@ cudaError_t launch_runs(const StoreFp8Args &a, cudaStream_t s) {
     const int64_t blocks =
         std::min((units(win, (H + heads - 1) / heads) + (q_units + W - 1) / W + groups - 1) / groups, resident);
     return launch_pdl(a.rotary_dim ? store_kv_fp8_kernel<D, W, C, true> : store_kv_fp8_kernel<D, W, C, false>,
-                      dim3((unsigned)blocks), dim3(THREADS), 0, s, a, win, (int)heads);
+                      dim3((unsigned)blocks), dim3(THREADS), 0, s, a, win, (int)heads, blocks == resident);
 }
 
 template <int D>
