@@ -17,9 +17,9 @@
 //   * With scores s_j (base 2) and V's exponents v_j, the sum is of 2^(x_j), x_j =
 //     s_j - a, and the product with V has the weights 2^(x_j + v_j - b), in fp16.
 //     The references a and b are whole numbers that follow the running maxima
-//     lazily: they leave the largest exponent at 8 and move when the weights'
-//     would pass 15 (or the sum's 60), so that a tile needs no reduction.  Weights
-//     down to 2^-22 of the largest keep fp16's 11 bits, and are gone below 2^-32.
+//     lazily: they leave the largest exponent between 7 and 8 and move when the
+//     weights' would pass 15 (or the sum's 60), so that a tile needs no reduction.
+//     Weights down to 2^-21 of the largest keep fp16's 11 bits, and are gone below 2^-32.
 //     Blocks whose scales are far apart need both references: with one, a zero
 //     block's 2^-120 would take its tokens out of the sum.  b is relative to a,
 //     for scores past 2^24 would swallow v_j.  Sums and accumulators are fp32.
