@@ -679,8 +679,9 @@ int minisgl_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const v
  * the row p = positions[i] of cos_sin_cache, [cos | sin]:
  *     y = x cos_j(p) - x' sin_j(p),   y' = x' cos_j(p) + x sin_j(p)   for the pair (x, x');
  * the other channels stay.  q is rounded to bf16 and written to q_out, which
- * may be q itself (same strides; else they must not overlap) and shares no
- * memory with k and v.  k is quantised from its fp32 rotation and left as it was.
+ * may be q itself (same strides; else no row of one may share memory with a row
+ * of the other, but they may be slices of one buffer) and shares no memory with
+ * k and v.  k is quantised from its fp32 rotation and left as it was.
  *   q, q_out: device bf16, [num_q_heads, head_dim] per token (token strides in
  *     elements, multiples of 8); num_q_heads may be 0, q then NULL.
  *   positions, out_loc: device int32 [n_tokens].

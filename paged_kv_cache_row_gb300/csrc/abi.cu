@@ -15,6 +15,7 @@
 
 #include "kernels.h"
 #include "minisgl.h"
+#include "rows_overlap.h"
 
 namespace {
 
@@ -988,12 +989,6 @@ int store_fp8_args(minisgl::StoreFp8Args &a, const char *who, const minisgl_kv_p
     return MINISGL_OK;
 }
 
-// Whether [a, a + na) and [b, b + nb) (in bytes) share memory.
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
 }  // namespace
 
 extern "C" {
@@ -1053,7 +1048,7 @@ int minisgl_rope_table(const uint64_t *turns, float attention, int32_t rotary_di
     if (n == 0) return MINISGL_OK;
     if (!positions || !out) return fail(MINISGL_ERR_ARG, "rope_table: NULL positions or out");
     if (!aligned16(out)) return fail(MINISGL_ERR_SHAPE, "rope_table: out must be 16-byte aligned");
-    if (overlap(positions, (int64_t)n * 4, out, (int64_t)n * rotary_dim * 4))
+    if (minisgl::overlap(positions, (int64_t)n * 4, out, (int64_t)n * rotary_dim * 4))
         return fail(MINISGL_ERR_ARG, "rope_table: out overlaps positions");
     minisgl::RopeTableArgs a = {};
     std::copy(turns, turns + rotary_dim / 2, a.turns);
@@ -1103,9 +1098,9 @@ int minisgl_rope_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, co
             return fail(MINISGL_ERR_SHAPE, "%s: q's token strides must be >= H_q*d and multiples of 8", who);
         if (n_tokens * (row / 8) >= (int64_t(1) << 31))
             return fail(MINISGL_ERR_UNSUPPORTED, "%s: n_tokens * H_q * d too large for one call", who);
-        const bool in_place = q == q_out && q_tok_stride == q_out_tok_stride;
-        if (!in_place && overlap(q, ((n_tokens - 1) * q_tok_stride + row) * 2, q_out,
-                                 ((n_tokens - 1) * q_out_tok_stride + row) * 2))
+        const minisgl::Rows from = {q, 2 * row, 2 * q_tok_stride}, to = {q_out, 2 * row, 2 * q_out_tok_stride};
+        const bool in_place = q == q_out && (n_tokens == 1 || q_tok_stride == q_out_tok_stride);
+        if (!in_place && minisgl::rows_overlap(from, to, n_tokens))
             return fail(MINISGL_ERR_ARG, "%s: q_out overlaps q without being q", who);
     }
     a.rotary_dim = rotary_dim;

@@ -429,6 +429,40 @@ def test_rope_store_with_a_steps_own_table():
     check_state(pools[0], pool_state(pools[1]))
 
 
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("first", ["q", "q_out"])
+def test_rope_store_into_another_slice_of_the_same_buffer(first, block):
+    """q, q_out, k and v are columns of one buffer, q before q_out and behind it."""
+    H, Hq, d, n = 2, 6, 64, 37
+    buf = kv_like((n, 2 * Hq + 2 * H, d), 4).to(DEV)
+    left, right, k, v = buf.split([Hq, Hq, H, H], 1)
+    q, q_out = (left, right) if first == "q" else (right, left)
+    kept = buf.clone()
+    pool, twin = new_pool(64, H, d, block), new_pool(64, H, d, block)
+    cache, rows = mk.minisgl_rope_table(mk.Rope(32), i32(range(100))), i32(range(7, 7 + n))
+    want = mk.minisgl_rope_store_kv_fp8(twin, 0, q.clone(), k.clone(), v.clone(), rows, cache, rows)
+    assert mk.minisgl_rope_store_kv_fp8(pool, 0, q, k, v, rows, cache, rows, q_out=q_out) is q_out
+    at = slice(Hq, 2 * Hq) if first == "q" else slice(0, Hq)
+    kept[:, at] = want
+    assert torch.equal(buf, kept)
+    check_state(pool, pool_state(twin))
+
+
+def test_rope_store_one_token_in_place_whatever_its_strides():
+    """The strides of one token mean nothing."""
+    pool, twin = new_pool(16, 2, 64, 16), new_pool(16, 2, 64, 16)
+    q, k, v = (kv_like((1, h, 64), h).to(DEV) for h in (4, 2, 3))
+    v = v[:, :2]
+    cache, at = mk.minisgl_rope_table(mk.Rope(64), i32(range(9))), i32([5])
+    want = mk.minisgl_rope_store_kv_fp8(twin, 0, q.clone(), k, v, at, cache, at)
+    lib = mk.load_library()
+    assert lib.minisgl_rope_store_kv_fp8(pool._ref, 0, q.data_ptr(), 4, 256, q.data_ptr(), 4096, k.data_ptr(),
+                                         v.data_ptr(), 128, 192, at.data_ptr(), cache.data_ptr(), 9, 64, 0, at.data_ptr(),
+                                         1, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(q, want)
+    check_state(pool, pool_state(twin))
+
+
 # --------------------------------------------------------------------------- #
 # load
 # --------------------------------------------------------------------------- #
