@@ -1102,6 +1102,10 @@ int minisgl_rope_store_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, co
         const bool in_place = q == q_out && (n_tokens == 1 || q_tok_stride == q_out_tok_stride);
         if (!in_place && minisgl::rows_overlap(from, to, n_tokens))
             return fail(MINISGL_ERR_ARG, "%s: q_out overlaps q without being q", who);
+        const int64_t kv_row = 2 * (int64_t)pool->num_kv_heads * pool->head_dim;
+        if (minisgl::rows_overlap({k, kv_row, 2 * k_tok_stride}, to, n_tokens) ||
+            minisgl::rows_overlap({v, kv_row, 2 * v_tok_stride}, to, n_tokens))
+            return fail(MINISGL_ERR_ARG, "%s: q_out overlaps k or v", who);
     }
     a.rotary_dim = rotary_dim;
     a.interleaved = interleaved != 0;

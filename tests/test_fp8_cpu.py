@@ -216,6 +216,19 @@ def test_rope_store_refusals(lib):
     assert b"rope_store_kv_fp8" in (call(3, -1), lib.minisgl_last_error())[1]
 
 
+def test_rope_store_refuses_queries_over_k_or_v(lib):
+    """q_out, q itself or not, on a row of k or of v: the first, the last, and by 16 bytes between two others."""
+    good = [ctypes.byref(_desc()), 0, FAKE, 16, 8192, 2 * FAKE, 8192, 3 * FAKE, 4 * FAKE, 8192, 8192, FAKE, FAKE, 99, 64, 0,
+            FAKE, 4, None]  # 4 KB of q and 2 KB of k and v, in rows of 16 KB
+    for i in (7, 8):
+        for out in (2 * FAKE, FAKE):
+            for off in (0, 4096 - 16, 16 - 2048, 3 * 16384 + 4000, -3 * 16384, 16384 + 16):
+                bad = list(good)
+                bad[5], bad[i] = out, out + off
+                assert lib.minisgl_rope_store_kv_fp8(*bad) == -1, (i, off)
+                assert b"q_out overlaps k or v" in lib.minisgl_last_error()
+
+
 def test_load_refusals(lib):
     call = _varied(lib.minisgl_load_kv_fp8, [ctypes.byref(_desc()), 0, FAKE, 4, 32, 32, FAKE, FAKE, 9, FAKE, FAKE, 1024,
                                              1024, None])
