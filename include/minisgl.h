@@ -586,6 +586,9 @@ int minisgl_decode_attn_fp4(const minisgl_kv_pool_fp4 *pool, int32_t layer, cons
  * minisgl_rope_frequencies (on the host; it touches no GPU) writes them as
  * turns[j] = frequency / (2 pi) * 2^64, rounded, and the factor of cos and sin:
  * attention_factor, or if that is 0 then 0.1 ln f + 1 for YARN and 1 otherwise.
+ * Frequencies are computed in double: turns[j] is within 2^-50 radians a position
+ * of its definition, for BANDS within 2^-49 fast_turns / (fast_turns - slow_turns)
+ * (its ramp magnifies roundings); lo and hi are those of x(t) in double.
  * rotary_dim: a multiple of 16, 16 .. 256.  factor >= 1 is not read for PLAIN;
  * original_positions, slow_turns and fast_turns (0 < slow < fast; usual are 1
  * and 4 for BANDS, 1 and 32 for YARN) are read for BANDS and YARN only.
@@ -609,8 +612,8 @@ int minisgl_rope_frequencies(const minisgl_rope *rope, uint64_t *turns, float *a
  * Rows of the table for positions [n]: with a_j = positions[i] * turns[j] / 2^64
  * turns, exact modulo one turn,
  *     out[i*rotary_dim + j] = attention * cos(a_j),  out[i*rotary_dim + rotary_dim/2 + j] = attention * sin(a_j).
- * cos and sin are within 2^-22 of the exact ones (times attention); the rounding
- * of turns adds at most |position| * 2^-53.  Positions may be any int32.  With
+ * cos and sin are within 2^-22 of those of a_j (times attention); what turns is off
+ * by (see above) moves a_j by |position| times as much.  Positions may be any int32.  With
  * positions 0, 1, 2, .. out is the table of the rotary calls; with a step's
  * positions it has a row for each token, whose position in those calls is then
  * its number.

@@ -1014,6 +1014,12 @@ int minisgl_rope_frequencies(const minisgl_rope *rope, uint64_t *turns, float *a
         return fail(MINISGL_ERR_ARG, "rope_frequencies: need 0 < slow_turns < fast_turns");
     const double m = rope->attention_factor != 0.0 ? rope->attention_factor : yarn ? 0.1 * std::log(f) + 1.0 : 1.0;
     if (!(m > 0.0 && m <= 1e6)) return fail(MINISGL_ERR_ARG, "rope_frequencies: attention_factor must be in [0, 1e6]");
+    // With u = 2^-53 and theta <= 1, a plain frequency is off by theta |ln theta| u <=
+    // 0.4 u (the exponent), 1.1 u (the power, within 0.53 units of its last place), 0.4 u
+    // (tau) and u (the quotient); by 2.4 u more where NTK changes the base, and by 5.5 u
+    // where two parts are summed: below 8 u = 2^-50.  The ramp of BANDS is off by
+    // 3.8 u t / (fast - slow) + 3.5 u: below 16 u fast / (fast - slow) in all.  Rounding to
+    // 2^-64 turns adds 2^-62.
     const double tau = 6.283185307179586476925286766559;
     if (rope->kind == MINISGL_ROPE_NTK) base *= std::pow(f, n / (n - 2.0));
     double lo = 0.0, hi = 0.0;

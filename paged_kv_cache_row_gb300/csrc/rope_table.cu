@@ -4,8 +4,9 @@
 // An angle matters modulo one turn, and fp32 loses it: at p = 10^6 a product
 // p * theta is off by up to 0.03.  So a frequency is a 64-bit fixed-point
 // number of turns, theta / 2 pi * 2^64, whose product with p modulo 2^64 is the
-// angle in turns modulo 1, exactly (the frequency's own rounding, in double,
-// moves the angle by at most p * 2^-53 of theta).  The two highest bits of the
+// angle in turns modulo 1, exactly (what the frequency itself is off by, computed
+// in double, moves the angle by at most p * 2^-50 radians, for frequencies in bands
+// by a small multiple).  The two highest bits of the
 // phase (rounded) are the quarter turn; cos and sin of the rest, at most pi/4,
 // are their Taylor polynomials up to x^10 and x^9, whose first terms left out
 // are below 2^-32 and 2^-29.

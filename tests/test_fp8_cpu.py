@@ -4,6 +4,7 @@ on the host), and the calls' refusals (checked on the host before any device
 work; the pointers are never dereferenced)."""
 import ctypes
 import math
+from decimal import Decimal, localcontext
 
 import numpy as np
 import pytest
@@ -95,6 +96,49 @@ def test_frequencies(lib, kind, rotary, base):
     assert np.abs(got - theta).max() <= 2.0 ** -60 + 2.0 ** -44
     assert (np.abs(got - theta) <= 2.0 ** -60 + 2.0 ** -44 * np.array(theta)).all()
     assert abs(rope.attention_factor - attention) <= 2.0 ** -23 * attention
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+def exact_frequencies(n, base, kind, factor, origin, slow, fast):
+    """The definition with 60 digits."""
+    with localcontext() as c:
+        c.prec = 60
+        base, f, origin, slow, fast = (Decimal(x) for x in (base, factor, origin, slow, fast))
+        if kind == "ntk":
+            base *= (f.ln() * n / (n - 2)).exp()
+        ln = base.ln()
+        if kind == "yarn":
+            at = [n * (origin / (2 * PI * t)).ln() / (2 * ln) for t in (fast, slow)]
+            lo, hi = max(0, math.floor(at[0])), min(n - 1, math.ceil(at[1]))
+            hi = hi if hi > lo else lo + Decimal("0.001")
+        out = []
+        for j in range(n // 2):
+            theta, s = (-2 * j * ln / n).exp(), Decimal(kind == "linear")
+            if kind == "bands":
+                s = 1 - min(Decimal(1), max(Decimal(0), (origin * theta / (2 * PI) - slow) / (fast - slow)))
+            if kind == "yarn":
+                s = min(Decimal(1), max(Decimal(0), Decimal(j - lo) / Decimal(hi - lo)))
+            out.append(s * theta / f + (1 - s) * theta)
+        return out
+
+
+@pytest.mark.parametrize("base", [1.5, 100.0, 10000.0, 500000.0, 1e6, 1e30])
+@pytest.mark.parametrize("kind,factor,origin,slow,fast", [
+    ("plain", 1.0, 0, 1, 32), ("linear", 3.7, 0, 1, 32), ("ntk", 8.0, 0, 1, 32), ("ntk", 1e6, 0, 1, 32),
+    ("bands", 8.0, 8192, 1, 4), ("bands", 7.7, 3.0, 1, 4), ("bands", 3.0, 100, 2.0, 2.001), ("yarn", 32.0, 4096, 1, 32),
+    ("yarn", 2.3, 2, 0.5, 0.6), ("yarn", 40.0, 100000, 1, 32)])
+def test_frequencies_are_as_near_as_the_header_says(lib, base, kind, factor, origin, slow, fast):
+    """Within 2^-50 radians a position, and for bands 2^-49 fast / (fast - slow)."""
+    bound = 2.0 ** -49 * fast / (fast - slow) if kind == "bands" else 2.0 ** -50
+    for n in (16, 48, 96, 128, 256):
+        turns = mk.Rope(n, base, kind, factor=factor, original_positions=origin, slow_turns=slow, fast_turns=fast).turns
+        want = exact_frequencies(n, base, kind, factor, origin, slow, fast)
+        with localcontext() as c:
+            c.prec = 60
+            off = [abs(Decimal(t) * 2 * PI / 2 ** 64 - w) for t, w in zip(turns, want)]
+        assert max(off) <= Decimal(bound), (n, off.index(max(off)), float(max(off)) * 2.0 ** 53)
 
 
 def test_frequency_scalings():
