@@ -19,7 +19,12 @@
 //     The references a and b are whole numbers that follow the running maxima
 //     lazily: they leave the largest exponent between 7 and 8 and move when the
 //     weights' would pass 15 (or the sum's 60), so that a tile needs no reduction.
-//     Weights down to 2^-21 of the largest keep fp16's 11 bits, and are gone below 2^-32.
+//     Weights down to 2^-21 of the largest keep fp16's 11 bits, and are gone below 2^-33.
+//     Why fp16: the product with V is an MMA whose other operand, the elements, is
+//     exact in it, and weights in two parts would take twice the MMAs.  bf16's rounding
+//     of the output hides it: against 64 bits the outputs of four batches are off by
+//     1.6e-3 to 1.7e-3 (of the norm), those of fp32 weights by the same (outputs of the
+//     two differ by 0.7e-3 to 1.2e-3, where a bf16 rounding falls the other way).
 //     Blocks whose scales are far apart need both references: with one, a zero
 //     block's 2^-120 would take its tokens out of the sum.  b is relative to a,
 //     for scores past 2^24 would swallow v_j.  Sums and accumulators are fp32.

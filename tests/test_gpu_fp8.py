@@ -705,6 +705,67 @@ def test_decode_scales_far_apart():
     assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want)).all() and np.abs(want).max() > 0
 
 
+def check_decode_closely(pool, q, table, lens, sm):
+    """check_decode with what is lost counted per output: a weight times its
+    block's 2^e is in fp16 with the largest of the request and head at 2^7 or
+    more, so it is off by 2^-11 of itself or by fp16's last half step, 2^-25:
+    2^-32 of the largest, times the element."""
+    (kc, ke), (vc, ve) = pool_state(pool)
+    k, v = ref.values(kc, ke, pool.block_tokens), ref.values(vc, ve, pool.block_tokens)
+    pt, G = table.cpu().numpy(), q.shape[1] // pool.num_kv_heads
+    n = np.asarray(lens)
+    got = f64(mk.minisgl_decode_attn_fp8(pool, 0, q, table, i32(lens), sm))
+    qq = f64(q)
+    want, mag, top = fp4_ref.decode(qq, k, v, pt, n, sm)
+    bound = fp4_ref.decode_bound(want, mag, top, 0.0, 0)
+    for r in range(len(n)):
+        rows = pt[r, :n[r]]
+        for h in range(q.shape[1]):
+            s = sm * k[rows, h // G] @ qq[r, h]
+            w = np.exp(s - s.max())
+            w *= 2.0 ** ve[rows // pool.block_tokens, h // G] / w.sum()
+            bound[r, h] += (1 + 2.0 ** -7) * 2.0 ** -32 * w.max() * np.abs(ref.value(vc[rows, h // G])).sum(0)
+    err = np.abs(got - want)
+    assert (err <= bound).all(), (float(err.max()), float((err - bound).max()))
+
+
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("power", [4, 12, 17, 20, 22, 26, 31, 40])
+def test_decode_an_outlier_in_one_channel(power, block):
+    """One channel of V is 2^power times the others in one block: the block's
+    tokens lose their other channels to the scale (at 2^-18 of the outlier), and
+    the other tokens keep theirs as far as fp16 weights under the larger scale do."""
+    d, n = 64, 96
+    k, v = kv_like((n, 2, d), 1), kv_like((n, 2, d), 2)
+    v[40, 0, 7] = 2.0 ** power
+    q = kv_like((3, 4, d), 3).to(DEV)
+    pool = new_pool(n, 2, d, block)
+    mk.minisgl_store_kv_fp8(pool, 0, k.to(DEV), v.to(DEV), i32(range(n)))
+    check_decode_closely(pool, q, i32([range(n)] * 3), [n, 32, 41], 0.125)
+
+
+@pytest.mark.parametrize("Hq,H,d,block", [(8, 2, 64, 16), (16, 8, 128, 1), (16, 1, 128, 64), (15, 5, 128, 32), (9, 3, 64, 1)])
+def test_decode_closely(Hq, H, d, block):
+    lens = [1, 31, 96, 33, 700, 64, 5, 129]
+    pool, q, table = case(len(lens), Hq, H, d, block, lens, Hq + H)
+    check_decode_closely(pool, q, table, lens, d ** -0.5)
+
+
+@pytest.mark.parametrize("huge", [1.0, 2.0 ** 40, 2.0 ** -100])
+def test_decode_scales_far_apart_closely(huge):
+    """Contexts without the block that is far larger are held to their own values."""
+    d, n, block = 64, 96, 16
+    k, v = kv_like((n, 1, d), 1), kv_like((n, 1, d), 2)
+    v[:16] = 0
+    v[16:32] *= 2.0 ** -60
+    k[32:48] = 0
+    v[80:] = (v[80:].double() * huge).to(torch.bfloat16)
+    pool = new_pool(n, 1, d, block)
+    mk.minisgl_store_kv_fp8(pool, 0, k.to(DEV), v.to(DEV), i32(range(n)))
+    q = kv_like((5, 2, d), 3).to(DEV)
+    check_decode_closely(pool, q, i32([range(n)] * 5), [n, 80, 32, 16, 17], 0.125)
+
+
 def test_decode_nan_stays_in_its_head():
     lens = [40, 100]
     pool, q, table = case(2, 8, 4, 64, 1, lens, 3)
