@@ -716,7 +716,7 @@ int minisgl_load_kv_fp8(const minisgl_kv_pool_fp8 *pool, int32_t layer, const in
  * pt_width <= 2^30.  Products accumulate in fp32; for the product with V a softmax
  * weight times its V block's scale is rounded to fp16: to 11 bits where it is at
  * least 2^-21 of the largest such product of the request and head, to within 2^-32
- * of that largest one below (so that what is below 2^-33 of it is lost).  Hence a
+ * of that largest one below (so that what is below 2^-32 of it may be lost).  Hence a
  * block of V whose scale is 2^21 times the others', for one outlier, takes bits
  * from the other tokens in every channel.  split_tokens and workspace: as for
  * minisgl_decode_attn_fp4 (splits count for a request and up to 8 KV heads

@@ -19,7 +19,7 @@
 //     The references a and b are whole numbers that follow the running maxima
 //     lazily: they leave the largest exponent between 7 and 8 and move when the
 //     weights' would pass 15 (or the sum's 60), so that a tile needs no reduction.
-//     Weights down to 2^-21 of the largest keep fp16's 11 bits, and are gone below 2^-33.
+//     Weights down to 2^-21 of the largest keep fp16's 11 bits, and may be gone below 2^-32.
 //     Why fp16: the product with V is an MMA whose other operand, the elements, is
 //     exact in it, and weights in two parts would take twice the MMAs.  bf16's rounding
 //     of the output hides it: against 64 bits the outputs of four batches are off by
