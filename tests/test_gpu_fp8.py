@@ -386,6 +386,13 @@ def test_rope_store(interleaved, rotary, d, block, in_place):
     assert np.array_equal(got[0], vc) and np.array_equal(got[1], ve)
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("rotary,d", [(16, 64), (48, 64), (64, 64), (32, 128), (112, 128), (128, 128)])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_rope_store_blocks_of_32(interleaved, rotary, d, in_place):
+    test_rope_store(interleaved, rotary, d, 32, in_place)
+
+
 def test_rope_store_is_the_bf16_calls_rotation():
     """Half-split pairs over the whole head: q as minisgl_rope_store_kv gives it, bit for bit."""
     H, Hq, d, n = 2, 8, 128, 50
