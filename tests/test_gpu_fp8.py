@@ -967,6 +967,67 @@ def test_calls_on_a_named_stream():
     assert torch.equal(got, want) and torch.equal(k, loaded[0]) and torch.equal(v, loaded[1])
 
 
+@pytest.mark.parametrize("block", [1, 16, 32])
+def test_stores_on_a_named_stream(block):
+    """Their rows are made on that stream, behind work that takes a while: a call on another stream would store what was there before."""
+    H, Hq, d, n = 3, 6, 64, 60
+    side = torch.cuda.Stream()
+    x = [kv_like((n, h, d), 10 + h).to(DEV) for h in (Hq, H, H)]
+    q, k, v = (torch.zeros_like(t) for t in x)
+    rows, cache = i32(range(4, 4 + n)), mk.minisgl_rope_table(mk.Rope(d), i32(range(99)))
+    pools = [new_pool(64, H, d, block) for _ in range(4)]
+    want = mk.minisgl_rope_store_kv_fp8(pools[0], 0, x[0].clone(), x[1], x[2], rows, cache, rows)
+    mk.minisgl_store_kv_fp8(pools[1], 0, x[1], x[2], rows)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        for a, b in zip((q, k, v), x):
+            a.copy_(b)
+    got = mk.minisgl_rope_store_kv_fp8(pools[2], 0, q, k, v, rows, cache, rows, stream=side)
+    mk.minisgl_store_kv_fp8(pools[3], 0, k, v, rows, stream=side)
+    side.synchronize()
+    assert got is q and torch.equal(q, want)
+    check_state(pools[2], pool_state(pools[0]))
+    check_state(pools[3], pool_state(pools[1]))
+
+
+@pytest.mark.parametrize("block", [1, 16, 32, 64])
+def test_captured_stores_and_load(block):
+    """Both stores and the load captured, and replayed while rows, values and lengths change in place."""
+    H, Hq, d, n, page = 3, 6, 128, 90, 64
+    rng = np.random.default_rng(block)
+    pools = [new_pool(20 * page, H, d, block, layers=2, page=page) for _ in range(2)]
+    cache = mk.minisgl_rope_table(mk.Rope(64), i32(range(20 * page)))
+    q, k, v, out = (torch.zeros((n, h, d), dtype=torch.bfloat16, device=DEV) for h in (Hq, H, H, Hq))
+    rows, pos, lens, off = i32(range(n)), i32(range(n)), i32([0, 0]), i32([0, 0, 0])
+    table, ko, vo = i32(np.zeros((2, n))), torch.zeros_like(k), torch.zeros_like(k)
+
+    def step(pool, q, k, v, out, ko, vo):
+        mk.minisgl_rope_store_kv_fp8(pool, 0, q, k, v, pos, cache, rows, interleaved=True, q_out=out)
+        mk.minisgl_store_kv_fp8(pool, 1, k, v, rows)
+        mk.minisgl_load_kv_fp8(pool, 1, table, lens, off, n, ko, vo)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(pools[0], q, k, v, out, ko, vo)
+    for turn in range(4):
+        a = int(rng.integers(1, n))  # two runs of rows in pages of their own
+        first = rng.permutation(9)[:2] * 2 * page + rng.integers(0, 30, 2)
+        r = np.concatenate([first[0] + np.arange(a), first[1] + np.arange(n - a)])
+        for t, x in ((rows, i32(r)), (pos, i32(rng.integers(0, 20 * page, n))), (lens, i32([a, n - a])), (off, i32([0, a, n]))):
+            t.copy_(x)
+        table[0, :a], table[1, :n - a] = rows[:a], rows[a:]
+        for t, h in ((q, Hq), (k, H), (v, H)):
+            t.copy_(kv_like((n, h, d), 10 * turn + h, 1.5 ** turn))
+        g.replay()
+        twin = [torch.empty_like(t) for t in (out, ko, vo)]
+        step(pools[1], q, k, v, *twin)
+        assert all(torch.equal(x, y) for x, y in zip((out, ko, vo), twin))
+        for layer in (0, 1):
+            check_state(pools[0], pool_state(pools[1], layer), layer)
+        assert np.array_equal(f64(ko), pool_values(pools[0], 1)[0][r])
+
+
 FIRST_USE_CAPTURED = """
 import torch, paged_kv_cache_row_gb300 as mk
 d = "cuda"
