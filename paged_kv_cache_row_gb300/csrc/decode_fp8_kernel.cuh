@@ -15,9 +15,7 @@
 // of all requests are cut evenly over the groups of all CTAs (split::Schedule).
 // At d 128, 8 heads, blocks of 4 make two groups, which load and compute in turns
 // of their own: 256 requests 224 us and 64 requests 58, where one block of 8
-// takes 228 and 60; blocks of 2 and of 1 make more partials and shorter copies
-// (230 and 253, 73 and 82).  At d 64 a block of 5, 6 or 7 heads takes 61, 62 and
-// 60 us where two blocks take 68, 66 and 65.
+// takes 228 and 60.  Other counts of heads: see block_heads.
 //
 // Loads: each group has a ring of three or more stages with a full and an
 // empty mbarrier each.  The group's warps fetch a tile together, each its run
@@ -35,14 +33,42 @@
 namespace minisgl {
 namespace fp8 {
 
-// KV heads of a block: blocks of one size, the last with what is left, of up to
-// 512 bytes a row.
+// KV heads of a block, up to 512 bytes of a row; the last block has what is left.
+// Times below are us for two batches of as many bytes whatever the heads (floors 45
+// and 210 us), with 4 query heads to a KV head.
+//
+// d 128: the largest of 4, 2 and 1 that leaves at most one warp in eight without a
+// head.  All 8 warps have to be in a group (two groups of 3 leave two out), and a warp
+// without a head still goes through its group's tiles.
+//   KV heads         3       5       6       7       8       9       10      13
+//   blocks of 4              70 285  63 249  60 233  58 226          60 237  61 243
+//   of 3             64 252          64 252                  63 253
+//   of 2             63 247  61 242  58 228  61 240  58 228  60 239  58 228  60 238
+//   of 1             61 238  60 239  62 253  62 252  62 252  62      62 252  62
+// (5 heads as 3 and 2: 71 294.  With 16 query heads 3, 5 and 6 KV heads take 70, 69 and
+// 67 us by the rule, and 80, 91 and 80 in blocks of 3.)
+//
+// d 64, where a head is 64 bytes of a row: one block of up to 8 heads, above that blocks
+// of 4 for an even count (every piece whole 128-byte lines), of one size for an odd one.
+//   KV heads         3       5       6       7       8       10      11      12      14      15
+//   one size, <= 8   60 234  61 239  62 241  61 237  58 224  63 266  66 267  61 240  61 253  61 251
+//   blocks of 4              68 305  66 288  65 279  59 224  60 239  64 276  57 226  60 239  64 278
+//   blocks of 2      78 348  74 341  61 240  72 337  59 235  60 240  72      - 252
+// (5, 6 and 7 heads as 3 and 2, 3 and 3, 4 and 3 in the second row.  With 16 query heads
+// blocks of 4 are better by 3 to 14 % for 12, 14 and 18, and worse by 3 for 10.)
 template <int D>
 constexpr int MOST_HEADS = 512 / D;
 template <int D>
 constexpr int block_heads(int num_kv_heads) {
-    const int blocks = (num_kv_heads + MOST_HEADS<D> - 1) / MOST_HEADS<D>;
-    return (num_kv_heads + blocks - 1) / blocks;
+    const auto blocks = [=](int heads) { return (num_kv_heads + heads - 1) / heads; };
+    if constexpr (D == 64) {
+        if (num_kv_heads > MOST_HEADS<D> && num_kv_heads % 2 == 0) return 4;
+        return blocks(blocks(MOST_HEADS<D>));
+    } else {
+        for (int heads = MOST_HEADS<D>; heads > 1; heads /= 2)
+            if ((blocks(heads) * heads - num_kv_heads) * 8 <= blocks(heads) * heads) return heads;
+        return 1;
+    }
 }
 
 }  // namespace fp8
@@ -120,8 +146,8 @@ __global__ void __launch_bounds__(MAX_WARPS<D> * 32, 1)
     const uint32_t ring = smem_u32(smem + lay.off_ring) + (uint32_t)(sub * stages) * stage_bytes;
     constexpr int v_off = HEADS * D, s_off = TILE * stride;
 
-    // This warp fetches tokens head_in * MINE .. of a tile (the last warp of three
-    // fewer); lane i holds the page-table entry of the tile's token i (past the end:
+    // This warp fetches tokens head_in * MINE .. of a tile (the last warp
+    // what is left); lane i holds the page-table entry of the tile's token i (past the end:
     // the last one's).
     constexpr int MINE = (TILE + HEADS - 1) / HEADS;
     const int32_t *table = nullptr;  // entry of the first token of the tile to fetch
@@ -471,16 +497,17 @@ cudaError_t launch_decode_fp8_as(const DecodeFp8Args &a, cudaStream_t s) {
     switch (fp8::block_heads<D>(a.d.num_kv_heads)) {
         case 1: return launch_cfg<D, NG, 1>(a, s);
         case 2: return launch_cfg<D, NG, 2>(a, s);
-        case 3: return launch_cfg<D, NG, 3>(a, s);
         case 4: return launch_cfg<D, NG, 4>(a, s);
         default: break;
     }
-    if constexpr (fp8::MOST_HEADS<D> > 4) {
+    if constexpr (D == 64) {
         switch (fp8::block_heads<D>(a.d.num_kv_heads)) {
+            case 3: return launch_cfg<D, NG, 3>(a, s);
             case 5: return launch_cfg<D, NG, 5>(a, s);
             case 6: return launch_cfg<D, NG, 6>(a, s);
             case 7: return launch_cfg<D, NG, 7>(a, s);
-            default: return launch_cfg<D, NG, 8>(a, s);
+            case 8: return launch_cfg<D, NG, 8>(a, s);
+            default: break;
         }
     }
     return cudaErrorInvalidValue;

@@ -582,6 +582,16 @@ def test_decode_head_layouts(Hq, H, d, block):
     check_decode(pool, q, table, lens, d ** -0.5)
 
 
+@pytest.mark.parametrize("G", [2, 9])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H", list(range(1, 19)) + [21, 32])
+def test_decode_every_count_of_heads(H, d, G):
+    """Blocks of heads of every size, and last blocks with one head less up to one head."""
+    lens = [1, 97, 0, 260]
+    pool, q, table = case(len(lens), G * H, H, d, 16, lens, H)
+    check_decode(pool, q, table, lens, d ** -0.5)
+
+
 @pytest.mark.parametrize("Hq,H,d", [(8, 2, 64), (16, 8, 128), (32, 2, 128), (11, 11, 128), (7, 7, 64)])
 def test_decode_short_tables(Hq, H, d):
     """Tables of one tile: streams are left whole, empty ones too."""
