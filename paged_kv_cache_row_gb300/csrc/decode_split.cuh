@@ -1,6 +1,7 @@
 // decode_split.cuh -- what the decode kernels of the quantised pools (4 and 8
-// bits) share: the cut of a batch's tiles into ranges, bounded waits on their
-// rings, and the kernel that joins split partials.
+// bits) share: the cut of a batch's tiles into ranges, the queries' layout and
+// bounded waits on their rings; and the kernel that joins the 4-bit decode's split
+// partials (the 8-bit one's are beside it).
 #pragma once
 #include <algorithm>
 #include <cstdint>
